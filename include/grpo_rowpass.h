@@ -81,6 +81,8 @@ typedef enum { GRPO_FP32 = 0, GRPO_BF16 = 1 } grpo_dtype;
  * the part of the row kept in shared memory).  Those outputs are not valid.  The kernel
  * returns without trapping (the GEMM with its TMEM freed). */
 #define GRPO_DEVERR_TIMEOUT 2
+/* A row's list of teacher ids holds a column twice (distill_topk_*). */
+#define GRPO_DEVERR_DUPLICATE_ID 4
 
 /* A [B, L, V] logits (or dlogits) tensor: ptr + b*stride_b + l*stride_l + j. */
 typedef struct {
@@ -457,6 +459,121 @@ grpo_status grpo_fused_linear_noalloc(const void* hidden, const void* weight, in
                                       float eps_low, float eps_high, int64_t chunk_rows, float* loss, float* logp,
                                       float* lse, float* kl, uint8_t* is_clipped, float* entropy, float* grad_hidden,
                                       float* grad_weight, int32_t* dev_err, grpo_stream_t stream);
+
+/*
+ * process_logits_fwd / process_logits_bwd -- the sampler's rules on logits, and their gradient.
+ *
+ * A sampler draws from processed logits: penalties for repeated tokens, biases, a grammar's
+ * mask.  The policy's log-probs in training are those of the same distribution, so the same
+ * rules run on every position there, with a gradient.  With s_j: column j occurs in the row's
+ * history, and n_j: how often it occurs among the history's generated tokens,
+ *
+ *   y_j  = x_j / repetition_b if s_j and x_j > 0,  x_j * repetition_b if s_j and x_j <= 0,
+ *          else x_j
+ *   y_j -= frequency_b * n_j + presence_b * [n_j > 0]
+ *   y_j += the bias listed for j
+ *   y_j  = -inf where the mask forbids j (whatever x_j is)
+ *
+ *   dx_j = dy_j * dy_j/dx_j: dy_j / repetition_b or dy_j * repetition_b as above, else dy_j,
+ *          and +0.0 where the mask forbids j (whatever dy_j is)
+ *
+ * computed in fp32 and rounded once to the logits' type.  Penalties, biases and masks are
+ * constants: only the logits have a gradient.  A row with nothing allowed is all -inf.
+ */
+typedef struct {
+  const int64_t* tokens;     /* [B][N] the sequences' tokens; NULL when N == 0.  A negative id is
+                                an empty place (padding) and is skipped */
+  int64_t tokens_stride;     /* elements between sequences, >= 0 (0: one history for all) */
+  int64_t N;                 /* 0 <= N < 2^19 */
+  const int32_t* hist_len;   /* [B*L] row r's history is its sequence's first hist_len[r] tokens;
+                                NULL = N.  Taken into [0, N]; outside sets the error bit */
+  const int32_t* prompt_len; /* [B] the first tokens are the prompt's: they count for repetition
+                                only; NULL = 0 */
+  const float* repetition;   /* [B] > 0, or NULL (no such penalty) */
+  const float* frequency;    /* [B] or NULL */
+  const float* presence;     /* [B] or NULL */
+  const int64_t* bias_ids;   /* [B][M]; a negative id is an unused entry.  Of a column listed twice
+                                the last entry counts */
+  const float* bias;         /* [B][M] */
+  int64_t M;                 /* 0 <= M < 2^12; 0: no biases, both pointers may be NULL */
+  const int32_t* allowed;    /* bitmask, or NULL: bit j % 32 of word j / 32 of a row is 1 where column
+                                j is allowed; ceil(V / 32) words a row (bits past V are ignored) */
+  int64_t allowed_stride_b;  /* words between sequences, >= 0 (0: the same mask) */
+  int64_t allowed_stride_l;  /* words between tokens, >= 0 (0: the same mask) */
+} grpo_logit_rules;
+
+/*
+ *   logits   [B, L, V] bf16 or fp32
+ *   rules    HOST struct as above; its arrays are device memory
+ *   out      [B, L, V] processed logits, same dtype and shape, its own strides (rows must not
+ *            overlap).  It may alias logits exactly: then only what the rules change is read
+ *            and written
+ *   dout     [B, L, V] gradient of the processed logits, same dtype and shape, its own strides
+ *   dlogits  [B, L, V] output like out; it may alias dout exactly, or logits exactly
+ * A token or bias id >= V sets GRPO_DEVERR_IDX_OUT_OF_RANGE and is skipped.  The history of a
+ * row is read in full only for the first row of a run of rows whose hist_len does not fall.
+ */
+grpo_status process_logits_fwd(const grpo_rows* logits, const grpo_logit_rules* rules, const grpo_rows* out,
+                               int32_t* dev_err, grpo_stream_t stream);
+grpo_status process_logits_bwd(const grpo_rows* logits, const grpo_rows* dout, const grpo_logit_rules* rules,
+                               const grpo_rows* dlogits, int32_t* dev_err, grpo_stream_t stream);
+
+/*
+ * topk_log_softmax -- the K largest log-probs of each row and their columns.
+ *
+ *   logits [B, L, V];  1 <= K <= min(V, GRPO_TOPK_MAX);  T > 0 finite
+ *   ids    [B*L][K] int64 output: columns by falling logit, ties by rising column (-0 equals +0)
+ *   logp   [B*L][K] fp32 output: x_id / T - lse
+ *   lse    [B*L] fp32 output, or NULL
+ * A row whose lse is not finite (a NaN or +inf logit, or nothing but -inf) has no log-probs:
+ * ids 0 .. K-1 and logp NaN, lse as it is.  Exact for every input; a row whose K-th largest
+ * value is shared by thousands of columns, or whose largest values come last, takes longer.
+ */
+#define GRPO_TOPK_MAX 256
+grpo_status topk_log_softmax(const grpo_rows* logits, int64_t K, float T, int64_t* ids, float* logp, float* lse,
+                             grpo_stream_t stream);
+
+/*
+ * distill_topk_fwd / _bwd / _fused -- distillation from a teacher's top log-probs.
+ *
+ * A row's divergence is taken over buckets: the listed columns, and the rest of the vocabulary
+ * as one more.  q: the teacher's probabilities of the buckets, p: the student's, from
+ * softmax(x / T) over the whole vocabulary.
+ *
+ *   loss_r = beta KL(q | m) + (1 - beta) KL(p | m),   m = beta q + (1 - beta) p,  0 < beta < 1;
+ *            KL(q | p) at beta = 0;  KL(p | q) at beta = 1
+ *   tail == 0: q_k is renormalised over the list (any shift of teacher_logp gives the same),
+ *              q_rest = 0;  beta must be < 1
+ *   tail != 0: q_k = exp(teacher_logp_k), q_rest = max(1 - sum q_k, 2^-20)
+ *   with G_b = p_b dloss/dp_b and S = sum_b G_b:
+ *   dlogits_rj = (dloss_r / T) (G_k - p_j S) at a listed column,
+ *                (dloss_r / T) p_j (G_rest / p_rest - S) at the others
+ *
+ *   logits        [B, L, V];  T > 0 finite;  0 <= beta <= 1
+ *   ids           [B*L][K] int64 listed columns, all different; a negative id is an unused
+ *                 slot.  1 <= K <= GRPO_DISTILL_MAX_K
+ *   teacher_logp  [B*L][K] fp32 (of unused slots not used)
+ *   mask          [B*L] uint8 or NULL: masked rows write +0.0 to every output, read no logits
+ *   loss, lse     [B*L] fp32 outputs;  p_rest: [B*L] fp32, the student's mass outside the list:
+ *                 the sum of exp(x_j / T - lse) over those columns, with the lse as stored (lse
+ *                 and p_rest are what the backward needs)
+ *   dloss         [B*L] fp32 upstream gradient of each row's loss
+ *   dlogits       as in grpo_loss_bwd (may alias logits exactly).  Rows that are masked or
+ *                 whose dloss_r / T is 0.0 are written as +0.0 without reading their logits
+ * An id >= V sets GRPO_DEVERR_IDX_OUT_OF_RANGE, an id listed twice GRPO_DEVERR_DUPLICATE_ID;
+ * such a row's loss, lse and p_rest are NaN, and with them its dlogits.
+ */
+#define GRPO_DISTILL_MAX_K 256
+grpo_status distill_topk_fwd(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                             const uint8_t* mask, float T, float beta, int32_t tail, float* loss, float* lse,
+                             float* p_rest, int32_t* dev_err, grpo_stream_t stream);
+grpo_status distill_topk_bwd(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                             const uint8_t* mask, const float* dloss, const float* lse, const float* p_rest, float T,
+                             float beta, int32_t tail, const grpo_rows* dlogits, grpo_stream_t stream);
+grpo_status distill_topk_fused(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                               const uint8_t* mask, const float* dloss, float T, float beta, int32_t tail,
+                               float* loss, float* lse, float* p_rest, const grpo_rows* dlogits, int32_t* dev_err,
+                               grpo_stream_t stream);
 
 /* A static, human-readable name for a status code (never NULL). */
 const char* grpo_status_string(grpo_status status);

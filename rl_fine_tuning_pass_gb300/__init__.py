@@ -7,6 +7,9 @@ generators.  The library is loaded on first use; importing the package needs no 
 """
 from .binding import (  # noqa: F401
     GrpoError,
+    distill_topk_bwd,
+    distill_topk_fused,
+    distill_topk_fwd,
     entropy_from_logits,
     entropy_from_logits_bwd,
     grpo_loss_bwd,
@@ -14,8 +17,17 @@ from .binding import (  # noqa: F401
     grpo_loss_fwd,
     grpo_seq_terms,
     load_library,
+    process_logits_bwd,
+    process_logits_fwd,
     selective_log_softmax_bwd,
     selective_log_softmax_fwd,
     status_string,
+    topk_log_softmax,
 )
-from .autograd import entropy, grpo_loss, selective_log_softmax  # noqa: F401,E402
+from .autograd import (  # noqa: F401,E402
+    distill_topk_loss,
+    entropy,
+    grpo_loss,
+    process_logits,
+    selective_log_softmax,
+)

@@ -7,6 +7,8 @@ library's entry points.  Marshalling only: every step runs in the CUDA kernels.
 * ``grpo_loss(logits, idx, adv, ...)``        -> per-token loss [B*L] (+ aux dict)
 * ``selective_log_softmax(logits, idx, T)``  -> logp [B*L]
 * ``entropy(logits, T)``                     -> H [B*L]
+* ``process_logits(logits, ...)``            -> logits under the sampler's rules
+* ``distill_topk_loss(logits, ids, logp)``   -> divergence from a teacher's top log-probs [B*L]
 
 Gradients flow to ``logits`` only (the other inputs are treated as constants, as in GRPO).
 The backward of ``grpo_loss`` receives d(objective)/d(loss_r) per token from autograd, which
@@ -16,6 +18,7 @@ is exactly the per-token ``dloss`` of grpo_loss_bwd.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as rp
 
@@ -91,3 +94,58 @@ class EntropyFunction(torch.autograd.Function):
 def entropy(logits, T=1.0):
     """Per-row entropy of softmax(logits / T), differentiable with respect to ``logits``."""
     return EntropyFunction.apply(logits, T)
+
+
+class ProcessLogitsFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, rules):
+        # tensors are kept by the graph, not by the context, so that a change in place between
+        # the passes is noticed
+        ctx.names = [k for k, v in rules.items() if v is not None]
+        ctx.save_for_backward(logits, *(rules[k] for k in ctx.names))
+        return rp.process_logits_fwd(logits, **rules)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        logits, *kept = ctx.saved_tensors
+        # autograd may hand over an expanded gradient, or one with another column stride
+        if dout.dtype != logits.dtype or dout.stride(-1) != 1 or dout.shape[-1] > 1 and 0 in dout.stride():
+            dout = dout.to(logits.dtype).contiguous()
+        return rp.process_logits_bwd(logits, dout, **dict(zip(ctx.names, kept))), None
+
+
+def process_logits(logits, *, tokens=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
+                   presence=None, bias_ids=None, bias=None, allowed=None):
+    """The logits under the sampler's rules (see process_logits_fwd), differentiable with
+    respect to ``logits``; penalties, biases and masks are constants."""
+    return ProcessLogitsFunction.apply(logits, dict(
+        tokens=tokens, hist_len=hist_len, prompt_len=prompt_len, repetition=repetition, frequency=frequency,
+        presence=presence, bias_ids=bias_ids, bias=bias, allowed=allowed))
+
+
+class DistillTopkFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, teacher_logp, mask, T, beta, tail):
+        out = rp.distill_topk_fwd(logits, ids, teacher_logp, T=T, beta=beta, tail=tail, mask=mask)
+        ctx.save_for_backward(logits, ids, teacher_logp, out["lse"], out["p_rest"],
+                              *(() if mask is None else (mask,)))
+        ctx.scalars = (T, beta, tail)
+        ctx.mark_non_differentiable(out["p_rest"])
+        return out["loss"], out["p_rest"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dloss, *unused):
+        logits, ids, tlogp, lse, p_rest, *mask = ctx.saved_tensors
+        T, beta, tail = ctx.scalars
+        dl = rp.distill_topk_bwd(logits, ids, tlogp, dloss.float().contiguous(), lse, p_rest, T=T, beta=beta, tail=tail,
+                                 mask=mask[0] if mask else None)
+        return dl, None, None, None, None, None, None
+
+
+def distill_topk_loss(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, mask=None):
+    """Per-row divergence [B*L] from a teacher's top log-probs (see distill_topk_fwd) and the
+    student's mass outside the list [B*L].  The loss is differentiable with respect to
+    ``logits``; the teacher is a constant."""
+    return DistillTopkFunction.apply(logits, ids, teacher_logp, mask, T, beta, tail)

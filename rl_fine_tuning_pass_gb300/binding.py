@@ -25,8 +25,12 @@ EXPORTED = ("grpo_loss_fwd", "grpo_loss_bwd", "grpo_loss_fused", "entropy_from_l
             "entropy_from_logits_bwd", "selective_log_softmax_fwd", "selective_log_softmax_bwd",
             "grpo_seq_terms", "grpo_vocab_shard_stats", "grpo_vocab_combine", "grpo_loss_bwd_vocab_shard",
             "selective_log_softmax_bwd_vocab_shard", "grpo_fused_linear_workspace_size", "grpo_fused_linear",
-            "grpo_fused_linear_noalloc", "grpo_status_string")
+            "grpo_fused_linear_noalloc", "grpo_status_string", "process_logits_fwd", "process_logits_bwd",
+            "topk_log_softmax", "distill_topk_fwd", "distill_topk_bwd", "distill_topk_fused")
 GRPO_VOCAB_MAX_WORLD = 64
+GRPO_DEVERR_DUPLICATE_ID = 4
+GRPO_TOPK_MAX = 256
+GRPO_DISTILL_MAX_K = 256
 
 
 class GrpoRows(ctypes.Structure):
@@ -34,6 +38,15 @@ class GrpoRows(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("B", ctypes.c_int64), ("L", ctypes.c_int64), ("V", ctypes.c_int64),
                 ("stride_b", ctypes.c_int64), ("stride_l", ctypes.c_int64)]
+
+
+class GrpoLogitRules(ctypes.Structure):
+    """Mirror of ``grpo_logit_rules``."""
+    _fields_ = [("tokens", ctypes.c_void_p), ("tokens_stride", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("hist_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("M", ctypes.c_int64), ("allowed", ctypes.c_void_p),
+                ("allowed_stride_b", ctypes.c_int64), ("allowed_stride_l", ctypes.c_int64)]
 
 
 class GrpoError(RuntimeError):
@@ -82,6 +95,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "grpo_fused_linear_noalloc": [_P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
                                       _P, _P, _P, _P, _F, _F, _F, _F, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P],
+        "process_logits_fwd": [rows_p, ctypes.POINTER(GrpoLogitRules), rows_p, _P, _P],
+        "process_logits_bwd": [rows_p, rows_p, ctypes.POINTER(GrpoLogitRules), rows_p, _P, _P],
+        "topk_log_softmax": [rows_p, ctypes.c_int64, _F, _P, _P, _P, _P],
+        "distill_topk_fwd": [rows_p, _P, _P, ctypes.c_int64, _P, _F, _F, ctypes.c_int32, _P, _P, _P, _P, _P],
+        "distill_topk_bwd": [rows_p, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _F, _F, ctypes.c_int32, rows_p, _P],
+        "distill_topk_fused": [rows_p, _P, _P, ctypes.c_int64, _P, _P, _F, _F, ctypes.c_int32, _P, _P, _P, rows_p, _P,
+                               _P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -439,3 +459,188 @@ def grpo_fused_linear(hidden, weight, idx, adv, dloss, *, B, L, T, beta, eps_low
         _stream(dev))
     _check("grpo_fused_linear", st)
     return {k: v for k, v in out.items() if v is not None}
+
+
+# ---------------------------------------------------------------------------
+# the sampler's rules on logits; a teacher's top log-probs; distillation from them
+# ---------------------------------------------------------------------------
+
+def _on(t: Optional[torch.Tensor], dtype, n: Optional[int], name: str, dev):
+    """``_ptr`` for a tensor that has to be on the logits' device."""
+    if t is None:
+        return None
+    p = _ptr(t, dtype, n, name)
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return p
+
+
+def _like(t: torch.Tensor, logits: torch.Tensor, name: str):
+    """A second [B, L, V] tensor of the call, described for C."""
+    if t.device != logits.device:
+        raise ValueError(f"{name} must be on {logits.device}, got {t.device}")
+    return rows_of(t)
+
+
+def _call(fn: str, dev, *args):
+    """Call the C entry point with the device's current stream, on that device."""
+    lib = load_library()
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(lib, fn)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib, fn)(*args, _stream(dev))
+    _check(fn, st)
+
+
+def _rules(B, L, V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed):
+    q = GrpoLogitRules()
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != B or tokens.dtype != torch.int64 or tokens.device != dev:
+            raise ValueError(f"tokens must be a [B, N] int64 tensor on {dev}")
+        if tokens.shape[1] > 1 and tokens.stride(1) != 1:
+            raise ValueError("tokens must have stride 1 along a sequence")
+        q.tokens, q.tokens_stride, q.N = tokens.data_ptr(), tokens.stride(0), tokens.shape[1]
+    elif hist_len is not None or prompt_len is not None or repetition is not None or frequency is not None \
+            or presence is not None:
+        raise ValueError("penalties and history lengths need tokens")
+    q.hist_len = _on(hist_len, torch.int32, B * L, "hist_len", dev)
+    q.prompt_len = _on(prompt_len, torch.int32, B, "prompt_len", dev)
+    q.repetition = _on(repetition, torch.float32, B, "repetition", dev)
+    q.frequency = _on(frequency, torch.float32, B, "frequency", dev)
+    q.presence = _on(presence, torch.float32, B, "presence", dev)
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias_ids is not None:
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != B or tuple(bias.shape) != tuple(bias_ids.shape):
+            raise ValueError("bias_ids and bias must be [B, M]")
+        q.bias_ids = _on(bias_ids, torch.int64, None, "bias_ids", dev)
+        q.bias = _on(bias, torch.float32, None, "bias", dev)
+        q.M = bias_ids.shape[1]
+    if allowed is not None:
+        words = (V + 31) // 32
+        if allowed.dim() == 2 and allowed.shape[0] == B * L:
+            sb, sl = L * allowed.stride(0), allowed.stride(0)
+        elif allowed.dim() == 3 and tuple(allowed.shape[:2]) == (B, L):
+            sb, sl = allowed.stride(0), allowed.stride(1)
+        else:
+            raise ValueError("allowed must be [B*L, W] or [B, L, W]")
+        if allowed.dtype != torch.int32 or allowed.device != dev:
+            raise ValueError(f"allowed must be an int32 tensor on {dev}")
+        if allowed.shape[-1] < words or (words > 1 and allowed.stride(-1) != 1):
+            raise ValueError(f"allowed needs {words} words a row, with stride 1")
+        q.allowed, q.allowed_stride_b, q.allowed_stride_l = allowed.data_ptr(), sb, sl
+    return q
+
+
+def process_logits_fwd(logits, *, tokens=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
+                       presence=None, bias_ids=None, bias=None, allowed=None, out=None, dev_err=None):
+    """The sampler's rules on [B, L, V] logits: penalties for the tokens [B, N] of each row's
+    history (the first hist_len[b*L + l] of its sequence, of which the first prompt_len[b]
+    count for repetition only), biases [B, M] on the columns bias_ids [B, M], and a bitmask of
+    the allowed columns, int32 [B*L, ceil(V / 32)] or [B, L, ceil(V / 32)] (expanded views
+    too).  A decode batch is [B, 1, V].  Returns the processed logits, allocated like logits
+    unless given; ``out=logits`` works in place and touches only what the rules change."""
+    B, L = _shape(logits)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dev = logits.device
+    x, y = rows_of(logits), _like(out, logits, "out")
+    q = _rules(B, L, x.V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed)
+    _call("process_logits_fwd", dev, ctypes.byref(x), ctypes.byref(q), ctypes.byref(y),
+          _on(dev_err, torch.int32, 1, "dev_err", dev))
+    return out
+
+
+def process_logits_bwd(logits, dout, *, tokens=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
+                       presence=None, bias_ids=None, bias=None, allowed=None, dlogits=None, dev_err=None):
+    """Gradient of the logits of process_logits_fwd from that of its output (dlogits allocated
+    like logits unless given; ``dlogits=dout`` works in place)."""
+    B, L = _shape(logits)
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dev = logits.device
+    x, dy, dx = rows_of(logits), _like(dout, logits, "dout"), _like(dlogits, logits, "dlogits")
+    q = _rules(B, L, x.V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed)
+    _call("process_logits_bwd", dev, ctypes.byref(x), ctypes.byref(dy), ctypes.byref(q), ctypes.byref(dx),
+          _on(dev_err, torch.int32, 1, "dev_err", dev))
+    return dlogits
+
+
+def topk_log_softmax(logits, K, *, T=1.0):
+    """The K largest log-probs of each row: (ids [B*L, K] int64, logp [B*L, K] fp32, lse [B*L]
+    fp32), by falling logit, ties by rising column.  1 <= K <= min(V, 256)."""
+    B, L = _shape(logits)
+    dev = logits.device
+    x = rows_of(logits)
+    K = int(K)
+    n = max(K, 0)
+    ids = torch.empty(B * L, n, dtype=torch.int64, device=dev)
+    logp = torch.empty(B * L, n, dtype=torch.float32, device=dev)
+    lse = torch.empty(B * L, dtype=torch.float32, device=dev)
+    _call("topk_log_softmax", dev, ctypes.byref(x), K, float(T), ids.data_ptr(), logp.data_ptr(), lse.data_ptr())
+    return ids, logp, lse
+
+
+def _list_of(logits, ids, teacher_logp, R):
+    if ids.dim() != 2 or ids.shape[0] != R or tuple(teacher_logp.shape) != tuple(ids.shape):
+        raise ValueError("ids and teacher_logp must be [B*L, K]")
+    dev = logits.device
+    return (_on(ids, torch.int64, None, "ids", dev), _on(teacher_logp, torch.float32, None, "teacher_logp", dev),
+            ids.shape[1])
+
+
+def distill_topk_fwd(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, mask=None, dev_err=None):
+    """Divergence of each row's softmax(logits / T) from a teacher's top log-probs (ids and
+    teacher_logp [B*L, K], K <= 256): dict with loss, lse and p_rest, each [B*L] fp32.
+    beta 0: KL(teacher | student), 1: KL(student | teacher), between: the mixture's.  tail:
+    the teacher's mass outside its list is one more bucket (needed at beta 1); without it the
+    teacher is renormalised over the list."""
+    B, L = _shape(logits)
+    R = B * L
+    dev = logits.device
+    x = rows_of(logits)
+    pi, pt, K = _list_of(logits, ids, teacher_logp, R)
+    out = {k: torch.empty(R, dtype=torch.float32, device=dev) for k in ("loss", "lse", "p_rest")}
+    _call("distill_topk_fwd", dev, ctypes.byref(x), pi, pt, K, _on(mask, torch.uint8, R, "mask", dev), float(T),
+          float(beta), int(bool(tail)), out["loss"].data_ptr(), out["lse"].data_ptr(), out["p_rest"].data_ptr(),
+          _on(dev_err, torch.int32, 1, "dev_err", dev))
+    return out
+
+
+def distill_topk_bwd(logits, ids, teacher_logp, dloss, lse, p_rest, *, T=1.0, beta=0.0, tail=False, mask=None,
+                     dlogits=None):
+    """dlogits of sum_r dloss_r * loss_r, with lse and p_rest of distill_topk_fwd (allocated
+    like logits unless given; ``dlogits=logits`` works in place)."""
+    B, L = _shape(logits)
+    R = B * L
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dev = logits.device
+    x, dx = rows_of(logits), _like(dlogits, logits, "dlogits")
+    pi, pt, K = _list_of(logits, ids, teacher_logp, R)
+    f = lambda t, name: _on(t, torch.float32, R, name, dev)  # noqa: E731
+    _call("distill_topk_bwd", dev, ctypes.byref(x), pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
+          f(dloss, "dloss"), f(lse, "lse"), f(p_rest, "p_rest"), float(T), float(beta), int(bool(tail)),
+          ctypes.byref(dx))
+    return dlogits
+
+
+def distill_topk_fused(logits, ids, teacher_logp, dloss, *, T=1.0, beta=0.0, tail=False, mask=None, dlogits=None,
+                       dev_err=None):
+    """distill_topk_fwd and distill_topk_bwd in one call, for loss weights dloss known in
+    advance; returns the forward's dict plus "dlogits"."""
+    B, L = _shape(logits)
+    R = B * L
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    dev = logits.device
+    x, dx = rows_of(logits), _like(dlogits, logits, "dlogits")
+    pi, pt, K = _list_of(logits, ids, teacher_logp, R)
+    out = {k: torch.empty(R, dtype=torch.float32, device=dev) for k in ("loss", "lse", "p_rest")}
+    _call("distill_topk_fused", dev, ctypes.byref(x), pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
+          _on(dloss, torch.float32, R, "dloss", dev), float(T), float(beta), int(bool(tail)), out["loss"].data_ptr(),
+          out["lse"].data_ptr(), out["p_rest"].data_ptr(), ctypes.byref(dx),
+          _on(dev_err, torch.int32, 1, "dev_err", dev))
+    out["dlogits"] = dlogits
+    return out

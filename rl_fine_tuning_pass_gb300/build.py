@@ -31,7 +31,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--ex
               "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["capi.cu", "rowpass_fwd_bf16.cu", "rowpass_fwd_f32.cu", "rowpass_bwd_bf16.cu", "rowpass_bwd_f32.cu",
            "rowpass_fused_bf16.cu", "rowpass_fused_f32.cu", "rowpass_seq.cu",
-           "rowpass_vocab.cu", "rowpass_linear.cu"]
+           "rowpass_vocab.cu", "rowpass_linear.cu", "rowpass_rules.cu", "rowpass_topk.cu", "rowpass_distill.cu"]
 
 
 def nvcc() -> str:

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "grpo_rowpass.h"
+#include "logits_ops.h"
 #include "rowpass_internal.h"
 #include "rowpass_linear.h"
 
@@ -625,6 +626,197 @@ const char* grpo_status_string(grpo_status status) {
     case GRPO_ERR_CUDA: return "GRPO_ERR_CUDA: the kernel launch failed";
     default: return "unknown grpo_status";
   }
+}
+
+}  // extern "C"
+
+namespace {
+
+// The rules' pointers and sizes for logits x; rows > 0.
+grpo_status check_rules(const grpo_logit_rules* q, const grpo_rows* x) {
+  if (q->N < 0 || q->M < 0 || q->tokens_stride < 0 || q->allowed_stride_b < 0 || q->allowed_stride_l < 0)
+    return GRPO_ERR_INVALID_ARG;
+  if (q->N > grpo::kRuleMaxTokens || q->M > grpo::kRuleMaxBias) return GRPO_ERR_UNSUPPORTED;
+  if (q->N > 0 && !ok_i64(q->tokens)) return GRPO_ERR_INVALID_ARG;
+  if (q->M > 0 && (!ok_i64(q->bias_ids) || !ok_f32(q->bias))) return GRPO_ERR_INVALID_ARG;
+  if (!aligned(q->hist_len, 4) || !aligned(q->prompt_len, 4) || !aligned(q->repetition, 4) ||
+      !aligned(q->frequency, 4) || !aligned(q->presence, 4) || !aligned(q->allowed, 4))
+    return GRPO_ERR_INVALID_ARG;
+  const long double far = static_cast<long double>(x->B) * q->tokens_stride +
+                          static_cast<long double>(x->B) * q->allowed_stride_b +
+                          static_cast<long double>(x->L) * q->allowed_stride_l;
+  return far > 1.0e18L ? GRPO_ERR_INVALID_ARG : GRPO_OK;
+}
+
+grpo::RulesParams rules_params(const grpo_rows* logits, const grpo_logit_rules* q, const grpo_rows* out,
+                               int32_t* dev_err) {
+  grpo::RulesParams p{};
+  p.x = view_of(logits);
+  p.out = grpo::OutView{out->ptr, out->L, out->stride_b, out->stride_l, static_cast<int>(out->V)};
+  // a history without penalties changes nothing
+  const bool counts = q->N > 0 && (q->repetition || q->frequency || q->presence);
+  p.tokens = counts ? q->tokens : nullptr;
+  p.tokens_stride = q->tokens_stride;
+  p.N = q->N;
+  p.hist_len = q->hist_len;
+  p.prompt_len = q->prompt_len;
+  p.repetition = q->repetition;
+  p.frequency = q->frequency;
+  p.presence = q->presence;
+  p.bias_ids = q->bias_ids;
+  p.bias = q->bias;
+  p.M = static_cast<int>(q->M);
+  p.allowed = reinterpret_cast<const uint32_t*>(q->allowed);
+  p.allowed_sb = q->allowed_stride_b;
+  p.allowed_sl = q->allowed_stride_l;
+  p.dev_err = dev_err;
+  return p;
+}
+
+bool same_tensor(const grpo_rows* a, const grpo_rows* b) {
+  return a->ptr == b->ptr && (a->B <= 1 || a->stride_b == b->stride_b) && (a->L <= 1 || a->stride_l == b->stride_l);
+}
+
+grpo_status check_distill(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K, float T,
+                          float beta, int32_t tail) {
+  grpo_status st = check_rows(logits);
+  if (st != GRPO_OK) return st;
+  if (!finite_pos(T) || !(beta >= 0.f && beta <= 1.f) || (beta == 1.f && tail == 0)) return GRPO_ERR_INVALID_ARG;
+  if (K < 1) return GRPO_ERR_INVALID_ARG;
+  if (K > grpo::kDistillMaxK) return GRPO_ERR_UNSUPPORTED;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  return ok_i64(ids) && ok_f32(teacher_logp) ? GRPO_OK : GRPO_ERR_INVALID_ARG;
+}
+
+grpo::DistillParams distill_params(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                                   const uint8_t* mask, float T, float beta, int32_t tail) {
+  grpo::DistillParams p{};
+  p.x = view_of(logits);
+  p.ids = ids;
+  p.tlogp = teacher_logp;
+  p.K = static_cast<int>(K);
+  p.mask = mask;
+  p.c = static_cast<float>(kLog2eD / static_cast<double>(T));
+  p.invT = 1.0 / static_cast<double>(T);
+  p.T = T;
+  p.beta = beta;
+  p.tail = tail != 0;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+grpo_status process_logits_fwd(const grpo_rows* logits, const grpo_logit_rules* rules, const grpo_rows* out,
+                               int32_t* dev_err, grpo_stream_t stream) {
+  grpo_status st = check_rows(logits);
+  if (st != GRPO_OK) return st;
+  bool same_phase = false;
+  if ((st = check_dlogits(logits, out, &same_phase)) != GRPO_OK) return st;
+  if (rules == nullptr) return GRPO_ERR_INVALID_ARG;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  if ((st = check_rules(rules, logits)) != GRPO_OK) return st;
+  if (!ok_opt_i32(dev_err)) return GRPO_ERR_INVALID_ARG;
+  const grpo::RulesParams p = rules_params(logits, rules, out, dev_err);
+  return from_cuda(grpo::launch_rules(logits->dtype, false, same_phase, same_tensor(logits, out), p, rows_of(logits),
+                                      device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+grpo_status process_logits_bwd(const grpo_rows* logits, const grpo_rows* dout, const grpo_logit_rules* rules,
+                               const grpo_rows* dlogits, int32_t* dev_err, grpo_stream_t stream) {
+  grpo_status st = check_rows(logits);
+  if (st != GRPO_OK) return st;
+  if ((st = check_rows(dout)) != GRPO_OK) return st;
+  if (dout->dtype != logits->dtype || dout->B != logits->B || dout->L != logits->L || dout->V != logits->V)
+    return GRPO_ERR_INVALID_ARG;
+  bool same_phase = false;
+  if ((st = check_dlogits(logits, dlogits, &same_phase)) != GRPO_OK) return st;
+  if ((st = check_dlogits(dout, dlogits, &same_phase)) != GRPO_OK) return st;
+  if (rules == nullptr) return GRPO_ERR_INVALID_ARG;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  if ((st = check_rules(rules, logits)) != GRPO_OK) return st;
+  if (!ok_opt_i32(dev_err)) return GRPO_ERR_INVALID_ARG;
+  grpo::RulesParams p = rules_params(logits, rules, dlogits, dev_err);
+  p.dy = view_of(dout);
+  return from_cuda(grpo::launch_rules(logits->dtype, true, same_phase, same_tensor(dout, dlogits), p, rows_of(logits),
+                                      device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+grpo_status topk_log_softmax(const grpo_rows* logits, int64_t K, float T, int64_t* ids, float* logp, float* lse,
+                             grpo_stream_t stream) {
+  grpo_status st = check_rows(logits);
+  if (st != GRPO_OK) return st;
+  if (!finite_pos(T) || K < 1 || K > logits->V) return GRPO_ERR_INVALID_ARG;
+  if (K > grpo::kTopkMax) return GRPO_ERR_UNSUPPORTED;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  if (!ok_i64(ids) || !ok_f32(logp) || !ok_opt_f32(lse)) return GRPO_ERR_INVALID_ARG;
+  grpo::TopkParams p{};
+  p.x = view_of(logits);
+  p.K = static_cast<int>(K);
+  p.c = static_cast<float>(kLog2eD / static_cast<double>(T));
+  p.invT = static_cast<float>(1.0 / static_cast<double>(T));
+  p.ids = ids;
+  p.logp = logp;
+  p.lse = lse;
+  return from_cuda(grpo::launch_topk(logits->dtype, p, rows_of(logits), device_sms(),
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+grpo_status distill_topk_fwd(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                             const uint8_t* mask, float T, float beta, int32_t tail, float* loss, float* lse,
+                             float* p_rest, int32_t* dev_err, grpo_stream_t stream) {
+  const grpo_status st = check_distill(logits, ids, teacher_logp, K, T, beta, tail);
+  if (st != GRPO_OK) return st;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  if (!ok_f32(loss) || !ok_f32(lse) || !ok_f32(p_rest) || !ok_opt_i32(dev_err)) return GRPO_ERR_INVALID_ARG;
+  grpo::DistillParams p = distill_params(logits, ids, teacher_logp, K, mask, T, beta, tail);
+  p.loss = loss;
+  p.lse = lse;
+  p.p_rest = p_rest;
+  p.dev_err = dev_err;
+  return from_cuda(grpo::launch_distill_fwd(logits->dtype, p, rows_of(logits), device_sms(),
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+grpo_status distill_topk_bwd(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                             const uint8_t* mask, const float* dloss, const float* lse, const float* p_rest, float T,
+                             float beta, int32_t tail, const grpo_rows* dlogits, grpo_stream_t stream) {
+  grpo_status st = check_distill(logits, ids, teacher_logp, K, T, beta, tail);
+  if (st != GRPO_OK) return st;
+  bool same_phase = false;
+  if ((st = check_dlogits(logits, dlogits, &same_phase)) != GRPO_OK) return st;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  if (!ok_f32(dloss) || !ok_f32(lse) || !ok_f32(p_rest)) return GRPO_ERR_INVALID_ARG;
+  grpo::DistillParams p = distill_params(logits, ids, teacher_logp, K, mask, T, beta, tail);
+  p.dx = grpo::OutView{dlogits->ptr, dlogits->L, dlogits->stride_b, dlogits->stride_l, static_cast<int>(dlogits->V)};
+  p.dloss = dloss;
+  p.lse = const_cast<float*>(lse);  // inputs of the backward
+  p.p_rest = const_cast<float*>(p_rest);
+  return from_cuda(grpo::launch_distill_bwd(logits->dtype, same_phase, p, rows_of(logits), device_sms(),
+                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+grpo_status distill_topk_fused(const grpo_rows* logits, const int64_t* ids, const float* teacher_logp, int64_t K,
+                               const uint8_t* mask, const float* dloss, float T, float beta, int32_t tail,
+                               float* loss, float* lse, float* p_rest, const grpo_rows* dlogits, int32_t* dev_err,
+                               grpo_stream_t stream) {
+  grpo_status st = check_distill(logits, ids, teacher_logp, K, T, beta, tail);
+  if (st != GRPO_OK) return st;
+  bool same_phase = false;
+  if ((st = check_dlogits(logits, dlogits, &same_phase)) != GRPO_OK) return st;
+  if (rows_of(logits) == 0) return GRPO_OK;
+  if (!ok_f32(dloss) || !ok_f32(loss) || !ok_f32(lse) || !ok_f32(p_rest) || !ok_opt_i32(dev_err))
+    return GRPO_ERR_INVALID_ARG;
+  grpo::DistillParams p = distill_params(logits, ids, teacher_logp, K, mask, T, beta, tail);
+  p.dx = grpo::OutView{dlogits->ptr, dlogits->L, dlogits->stride_b, dlogits->stride_l, static_cast<int>(dlogits->V)};
+  p.dloss = dloss;
+  p.loss = loss;
+  p.lse = lse;
+  p.p_rest = p_rest;
+  p.dev_err = dev_err;
+  return from_cuda(grpo::launch_distill_fused(logits->dtype, same_phase, p, rows_of(logits), device_sms(),
+                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
