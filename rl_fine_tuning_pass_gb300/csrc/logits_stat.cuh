@@ -49,11 +49,33 @@ __device__ __forceinline__ void maxrun_sum(MaxRun& r, const uint4 (&v)[N], float
     }
 }
 
-// Fold vectors in; returns their largest element.
+// Largest element of the vectors' even and of their odd places (NaN loses against a number).
+template <int N>
+__device__ __forceinline__ float2 pair_max(const uint4 (&v)[N], BF16*) {
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v[k]);
+    m = __hmax2(m, __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+  }
+  return make_float2(__low2float(m), __high2float(m));
+}
+template <int N>
+__device__ __forceinline__ float2 pair_max(const uint4 (&v)[N], F32*) {
+  float2 m = make_float2(__uint_as_float(v[0].x), __uint_as_float(v[0].y));
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    m.x = fmaxf(m.x, fmaxf(__uint_as_float(v[k].x), __uint_as_float(v[k].z)));
+    m.y = fmaxf(m.y, fmaxf(__uint_as_float(v[k].y), __uint_as_float(v[k].w)));
+  }
+  return m;
+}
+
+// Fold vectors in; returns pair_max of them.
 template <class E, int N>
-__device__ __forceinline__ float maxrun_vectors(MaxRun& r, const uint4 (&v)[N], float c) {
-  const float m = E::template chunk_max<N>(v);
-  maxrun_raise(r, m, c);
+__device__ __forceinline__ float2 maxrun_vectors(MaxRun& r, const uint4 (&v)[N], float c) {
+  const float2 m = pair_max(v, static_cast<E*>(nullptr));
+  maxrun_raise(r, fmaxf(m.x, m.y), c);
   maxrun_sum<E, N>(r, v, c);
   return m;
 }

@@ -1,10 +1,19 @@
 // The K largest log-probs of each row, log_softmax(x / T), with their columns: sorted, ties
 // to the lowest column.
 //
-// A row is streamed once for the softmax statistic (logits_stat.cuh); the K largest are
-// then found by radix selection on order-preserving keys of the logits: 8 bits of the key per
-// sweep (two sweeps for bf16, four for fp32), then one sweep that collects the columns above
-// the K-th key and one, in column order, that takes the ties.
+// One sweep over the row forms the softmax statistic (logits_stat.cuh) and collects the
+// candidates.  Each thread keeps the largest element it has met in the even and in the odd
+// places of its vectors, 512 maxima per CTA; the K-th largest of those maxima is a lower bound of
+// the K-th largest element seen so far (K different elements reach it), so an element below it
+// cannot be a result.  The bound is taken anew after 1, 2, 4, 8, ... steps of the sweep: of N(0, 1)
+// elements about 70 of the first step pass it at K = 64, and as many of each doubling, some 360 of a
+// row of 151936.  Those that also pass the last bound (about 70) are ranked by counting.
+//
+// Rows that collect more than the buffers hold (thousands of ties at the K-th value, large
+// values that come last) are done again by radix selection on order-preserving keys.
+//
+// With few rows, a cluster of CTAs takes a row: each CTA ranks its own part, the first one
+// merges the sorted lists and the statistics, which the others write into its shared memory.
 #include "logits_ops.h"
 #include "logits_stat.cuh"
 
@@ -45,12 +54,43 @@ __device__ __forceinline__ void for_row(const typename E::storage* row, int V, F
   }
 }
 
+// The first `need` columns, in column order, whose key >> shift is `key`, into list.
+template <class E>
+__device__ void fill_ties(const typename E::storage* row, int V, uint32_t key, int shift, unsigned need,
+                          uint64_t* list) {
+  __shared__ unsigned wsum[kTopkThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned done = 0;
+  for (int j0 = 0; j0 < V && done < need; j0 += kTopkThreads) {
+    const int j = j0 + tid;
+    uint32_t k = 0u;
+    bool tie = false;
+    if (j < V) {
+      k = key_of(E::load_scalar(row + j));
+      tie = (k >> shift) == key;
+    }
+    const unsigned bal = __ballot_sync(0xFFFFFFFFu, tie);
+    if (lane == 0) wsum[warp] = __popc(bal);
+    __syncthreads();
+    unsigned at = done + __popc(bal & ((1u << lane) - 1u));
+    unsigned total = 0;
+#pragma unroll
+    for (int w = 0; w < kTopkThreads / 32; ++w) {
+      if (w < warp) at += wsum[w];
+      total += wsum[w];
+    }
+    if (tie && at < need) list[at] = entry_of(k, j);
+    done += total;
+    __syncthreads();
+  }
+  __syncthreads();
+}
+
 // Radix selection of the K largest entries of the row into list[0..K) (any order).
 template <class E>
 __device__ void radix_select(const typename E::storage* row, int V, int K, uint64_t* list) {
   __shared__ unsigned hist[256];
   __shared__ unsigned sh_digit, sh_above, sh_n;
-  __shared__ unsigned wsum[kTopkThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kPasses = sizeof(typename E::storage);  // the key's low half is fixed for bf16
   uint32_t prefix = 0u;
@@ -96,64 +136,170 @@ __device__ void radix_select(const typename E::storage* row, int V, int K, uint6
     const uint32_t k = key_of(x);
     if ((k >> kShift) > prefix) list[atomicAdd(&sh_n, 1u)] = entry_of(k, j);
   });
-  // the ties, in column order
-  unsigned done = 0;
-  for (int j0 = 0; j0 < V && done < need; j0 += kTopkThreads) {
-    const int j = j0 + tid;
-    uint32_t k = 0u;
-    bool tie = false;
-    if (j < V) {
-      k = key_of(E::load_scalar(row + j));
-      tie = (k >> kShift) == prefix;
-    }
-    const unsigned bal = __ballot_sync(0xFFFFFFFFu, tie);
-    if (lane == 0) wsum[warp] = __popc(bal);
-    __syncthreads();
-    unsigned at = done + __popc(bal & ((1u << lane) - 1u));
-    unsigned total = 0;
-#pragma unroll
-    for (int w = 0; w < kTopkThreads / 32; ++w) {
-      if (w < warp) at += wsum[w];
-      total += wsum[w];
-    }
-    if (tie && at < need) list[K - need + at] = entry_of(k, j);
-    done += total;
-    __syncthreads();
-  }
   __syncthreads();
+  fill_ties<E>(row, V, prefix, kShift, need, list + (K - need));
 }
 
-template <class E>
-__global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p) {
+constexpr int kMaxima = 2 * kTopkThreads;   // running maxima per CTA
+constexpr int kSurvivors = 1024;            // entries ranked by counting
+constexpr uint32_t kKeyNegInf = 0x007Fu;    // high half of the key of -inf
+
+// High half of the K-th largest of the CTA's running maxima (keys in sh; warp 0 only).
+__device__ __forceinline__ uint32_t kth_maximum(const uint16_t* sh, int K) {
+  const int lane = threadIdx.x;
+  uint32_t k[kMaxima / 32];
+#pragma unroll
+  for (int q = 0; q < kMaxima / 32; ++q) k[q] = sh[lane + 32 * q];
+  uint32_t best = 0u;
+#pragma unroll 1
+  for (uint32_t bit = 0x8000u; bit != 0u; bit >>= 1) {
+    const uint32_t cand = best | bit;
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxima / 32; ++q) n += k[q] >= cand;
+    if (__reduce_add_sync(0xFFFFFFFFu, n) >= K) best = cand;
+  }
+  return best;
+}
+
+struct TopkPart {  // what one CTA of a cluster hands to the first
+  float m, s;
+  int n;           // entries in its list, -1: its buffers overflowed
+};
+
+// CS CTAs per row (a cluster when CS > 1).  Dynamic shared memory: cap candidates, then
+// kSurvivors, then (CS > 1) the CTAs' lists.
+template <class E, int CS>
+__global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p, int cap) {
   using S = typename E::storage;
-  wait_for_previous_grids();
+  constexpr int VEC = E::kVec, T = kTopkThreads, U = kUnroll;
+  extern __shared__ uint64_t topk_smem[];
+  __shared__ uint16_t maxima[kMaxima];
   __shared__ uint64_t list[kTopkMax];
-  __shared__ float sh_m, sh_ln_s, sh_lse;
-  const int64_t r = blockIdx.x;
+  __shared__ TopkPart parts[CS];
+  __shared__ float sh_thr;
+  __shared__ unsigned sh_n, sh_m;
+  uint64_t* cand = topk_smem;
+  uint64_t* surv = topk_smem + cap;
+  uint64_t* lists = surv + kSurvivors;
+  if (CS > 1) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
+  wait_for_previous_grids();
+  const uint32_t rank = CS > 1 ? cluster_rank() : 0u;
+  const int64_t r = blockIdx.x / CS;
   const int64_t b = r / p.x.L, l = r - b * p.x.L;
   const S* row = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
   const int V = p.x.V, K = p.K, tid = threadIdx.x;
   const float c = p.c;
+  const RowSplit sp = split_row<E>(row, V);
+  const int part = (sp.nvec + CS - 1) / CS;
+  const int v0 = min(sp.nvec, static_cast<int>(rank) * part), v1 = min(sp.nvec, v0 + part);
+  if (tid == 0) sh_n = sh_m = 0u;
+  __syncthreads();
 
   MaxRun rs;
-  const RowSplit sp = split_row<E>(row, V);
-  if (tid < sp.head) maxrun_scalar(rs, E::load_scalar(row + tid), c);
-  if (tid < sp.tail) maxrun_scalar(rs, E::load_scalar(row + sp.head + sp.nvec * E::kVec + tid), c);
+  float2 sub = make_float2(-INFINITY, -INFINITY);
+  auto take = [&](float x, int j) {
+    const unsigned at = atomicAdd(&sh_n, 1u);
+    if (at < static_cast<unsigned>(cap)) cand[at] = entry_of(key_of(x), j);
+  };
+  auto scalar = [&](int j) {
+    const float x = E::load_scalar(row + j);
+    maxrun_scalar(rs, x, c);
+    sub.x = fmaxf(sub.x, x);
+    if (x > -INFINITY) take(x, j);
+  };
+  if (rank == 0 && tid < sp.head) scalar(tid);
+  if (rank == CS - 1 && tid < sp.tail) scalar(sp.head + sp.nvec * VEC + tid);
+
+  float thr = -INFINITY;
+  auto bound = [&]() {  // a new bound from the maxima so far
+    maxima[tid] = static_cast<uint16_t>(key_of(sub.x) >> 16);
+    maxima[T + tid] = static_cast<uint16_t>(key_of(sub.y) >> 16);
+    __syncthreads();
+    if (tid < 32) {
+      const uint32_t k = kth_maximum(maxima, K);
+      if (tid == 0) sh_thr = k <= kKeyNegInf ? -INFINITY : value_of(k << 16);
+    }
+    __syncthreads();
+    thr = sh_thr;
+  };
   const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
-  int i = tid;
-  for (; i + (kUnroll - 1) * kTopkThreads < sp.nvec; i += kUnroll * kTopkThreads) {
-    uint4 v[kUnroll];
+  const uint32_t pad = sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  int step = 0, next = 1;
+  for (int i0 = v0; i0 < v1; i0 += U * T) {
+    uint4 v[U];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) v[k] = ld_nc_v4(vb + i + k * kTopkThreads);
-    maxrun_vectors<E>(rs, v, c);
+    for (int k = 0; k < U; ++k) {
+      const int i = i0 + k * T + tid;
+      v[k] = i < v1 ? ld_nc_v4(vb + i) : make_uint4(pad, pad, pad, pad);
+    }
+    const float2 pm = maxrun_vectors<E>(rs, v, c);
+    sub.x = fmaxf(sub.x, pm.x);
+    sub.y = fmaxf(sub.y, pm.y);
+    if (++step == next) {
+      bound();
+      next *= 2;
+    }
+    const float m = fmaxf(pm.x, pm.y);
+    if (m >= thr && m > -INFINITY) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const uint4 one[1] = {v[k]};
+        const float2 mk = pair_max(one, static_cast<E*>(nullptr));
+        if (fmaxf(mk.x, mk.y) < thr) continue;
+        float f[VEC];
+        E::unpack(v[k], f);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q)
+          if (f[q] >= thr && f[q] > -INFINITY) take(f[q], sp.head + (i0 + k * T + tid) * VEC + q);
+      }
+    }
   }
-  for (; i < sp.nvec; i += kTopkThreads) {
-    const uint4 v[1] = {ld_nc_v4(vb + i)};
-    maxrun_vectors<E>(rs, v, c);
+  if (step * 2 != next) bound();  // elements since the last bound
+  MaxStat st = maxstat_block<T>(rs.stat(), c);
+  __syncthreads();
+
+  // the candidates that pass the last bound
+  const unsigned n = sh_n;
+  const uint64_t least = entry_of(key_of(thr), 0x7FFFFFFF);
+  for (unsigned i = tid; i < min(n, static_cast<unsigned>(cap)); i += T) {
+    const uint64_t e = cand[i];
+    if (e >= least) {
+      const unsigned at = atomicAdd(&sh_m, 1u);
+      if (at < kSurvivors) surv[at] = e;
+    }
   }
-  const MaxStat st = maxstat_block<kTopkThreads>(rs.stat(), c);
+  __syncthreads();
+  int m = static_cast<int>(sh_m);
+  const bool over = n > static_cast<unsigned>(cap) || m > kSurvivors;
+  uint64_t* mine = list;
+  if (CS > 1) {
+    cluster_wait();
+    // this CTA's sorted list, in the first CTA's shared memory
+    const uint32_t at = map_to_rank(smem_addr(lists + rank * static_cast<uint32_t>(K)), 0);
+    for (int i = tid; !over && i < m; i += T) {
+      const uint64_t e = surv[i];
+      int place = 0;
+      for (int q = 0; q < m; ++q) place += surv[q] > e;
+      if (place < K) st_cluster_u64(at + 8u * place, e);
+    }
+    if (tid == 0) {
+      const uint32_t to = map_to_rank(smem_addr(&parts[rank]), 0);
+      st_cluster_f32(to, st.m);
+      st_cluster_f32(to + 4u, st.s);
+      st_cluster_f32(to + 8u, __int_as_float(over ? -1 : min(m, K)));
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    if (tid < 32) {
+      st = tid < CS ? MaxStat{parts[tid].m, parts[tid].s} : MaxStat{-FLT_MAX, 0.f};
+      st = maxstat_warp(st, c);
+    }
+  }
+
+  __shared__ float sh_max, sh_ln_s, sh_lse;
   if (tid == 0) {
-    sh_m = st.m;
+    sh_max = st.m;
     sh_ln_s = logf(st.s);
     sh_lse = fmaf(st.m, p.invT, sh_ln_s);
     if (p.lse) p.lse[r] = sh_lse;
@@ -161,30 +307,118 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p) 
   __syncthreads();
   int64_t* ids = p.ids + r * K;
   float* logp = p.logp + r * K;
-  if (!isfinite(sh_lse)) {  // a NaN or +inf logit, or nothing but -inf: no log-prob is defined
-    for (int k = tid; k < K; k += kTopkThreads) {
+  const float ln_s = sh_ln_s, xmax = sh_max;
+  if (!(fabsf(ln_s) <= FLT_MAX)) {  // a NaN or +inf logit, or nothing but -inf: no log-prob is defined
+    for (int k = tid; k < K; k += T) {
       ids[k] = k;
       logp[k] = __int_as_float(0x7FC00000);
     }
     return;
   }
-  radix_select<E>(row, V, K, list);
-  for (int k = tid; k < K; k += kTopkThreads) {  // each entry's rank is its place
-    const uint64_t e = list[k];
-    int rank = 0;
-    for (int q = 0; q < K; ++q) rank += list[q] > e;
-    ids[rank] = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
-    logp[rank] = fmaf(value_of(static_cast<uint32_t>(e >> 32)) - sh_m, p.invT, -sh_ln_s);
+  auto put = [&](int place, uint64_t e) {
+    ids[place] = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(e));
+    logp[place] = fmaf(value_of(static_cast<uint32_t>(e >> 32)) - xmax, p.invT, -ln_s);
+  };
+  int have = m;        // entries that are ranked below or in the lists
+  bool again = over;
+  if (CS > 1) {
+    have = 0;
+#pragma unroll
+    for (int q = 0; q < CS; ++q) {
+      again |= parts[q].n < 0;
+      have += parts[q].n;
+    }
+  }
+  if (again) {  // too many candidates: by radix selection
+    radix_select<E>(row, V, K, mine);
+    for (int k = tid; k < K; k += T) {
+      const uint64_t e = mine[k];
+      int place = 0;
+      for (int q = 0; q < K; ++q) place += mine[q] > e;
+      put(place, e);
+    }
+    return;
+  }
+  if (have < K) {  // fewer than K columns above -inf: the first of the others follow them
+    const uint32_t key = key_of(-INFINITY);
+    fill_ties<E>(row, V, key, 0, static_cast<unsigned>(K - have), mine);
+    for (int k = tid; k < K - have; k += T) put(have + k, mine[k]);
+  }
+  if (CS == 1) {
+    for (int i = tid; i < m; i += T) {
+      const uint64_t e = surv[i];
+      int place = 0;
+      for (int q = 0; q < m; ++q) place += surv[q] > e;
+      if (place < K) put(place, e);
+    }
+  } else {
+    for (int i = tid; i < CS * K; i += T) {
+      const int from = i / K, at = i - from * K;
+      if (at >= parts[from].n) continue;
+      const uint64_t e = lists[i];
+      int place = at;
+#pragma unroll 1
+      for (int q = 0; q < CS; ++q) {  // how many of list q are larger: a binary search
+        if (q == from) continue;
+        int lo = 0, hi = parts[q].n;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (lists[q * K + mid] > e) lo = mid + 1;
+          else hi = mid;
+        }
+        place += lo;
+      }
+      if (place < K) put(place, e);
+    }
+  }
+}
+
+// CTAs per row: as many as keep all CTAs resident at once (4 of 256 threads per SM), each with
+// a step of the sweep (1024 vectors) or more.
+template <class E>
+int pick_split(const TopkParams& p, int64_t rows, int sms) {
+  int cs = 1;
+  while (cs < 8 && rows * cs * 2 <= 4LL * sms && p.x.V / E::kVec >= 1024 * cs) cs *= 2;
+  return cs;
+}
+
+template <class E, int CS>
+cudaError_t launch_topk_cs(const TopkParams& p, int64_t rows, cudaStream_t s) {
+  const int cap = p.K > 128 ? 4096 : 2048;
+  const size_t smem = 8 * (static_cast<size_t>(cap) + kSurvivors + (CS > 1 ? CS * p.K : 0));
+  const cudaError_t e = cudaFuncSetAttribute(topk_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             8 * (4096 + kSurvivors + (CS > 1 ? CS * kTopkMax : 0)));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * CS));
+  cfg.blockDim = dim3(kTopkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, topk_kernel<E, CS>, p, cap);
+}
+
+template <class E>
+cudaError_t launch_topk_e(const TopkParams& p, int64_t rows, int sms, cudaStream_t s) {
+  switch (pick_split<E>(p, rows, sms)) {
+    case 8: return launch_topk_cs<E, 8>(p, rows, s);
+    case 4: return launch_topk_cs<E, 4>(p, rows, s);
+    case 2: return launch_topk_cs<E, 2>(p, rows, s);
+    default: return launch_topk_cs<E, 1>(p, rows, s);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_topk(int dtype, const TopkParams& p, int64_t rows, int sms, cudaStream_t stream) {
-  (void)sms;
-  const dim3 grid(static_cast<unsigned>(rows)), block(kTopkThreads);
-  return dtype == 1 ? launch_after_previous(topk_kernel<BF16>, grid, block, stream, p)
-                    : launch_after_previous(topk_kernel<F32>, grid, block, stream, p);
+  return dtype == 1 ? launch_topk_e<BF16>(p, rows, sms, stream) : launch_topk_e<F32>(p, rows, sms, stream);
 }
 
 }  // namespace grpo
