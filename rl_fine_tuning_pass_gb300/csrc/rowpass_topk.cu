@@ -1,13 +1,15 @@
 // The K largest log-probs of each row, log_softmax(x / T), with their columns: sorted, ties
 // to the lowest column.
 //
-// One sweep over the row forms the softmax statistic (logits_stat.cuh) and collects the
-// candidates.  Each thread keeps the largest element it has met in the even and in the odd
+// One sweep over the row forms the softmax statistic (logits_stat.cuh) and notes where
+// candidates are.  Each thread keeps the largest element it has met in the even and in the odd
 // places of its vectors, 512 maxima per CTA; the K-th largest of those maxima is a lower bound of
-// the K-th largest element seen so far (K different elements reach it), so an element below it
-// cannot be a result.  The bound is taken anew after 1, 2, 4, 8, ... steps of the sweep: of N(0, 1)
-// elements about 70 of the first step pass it at K = 64, and as many of each doubling, some 360 of a
-// row of 151936.  Those that also pass the last bound (about 70) are ranked by counting.
+// the K-th largest element seen so far (K different elements reach it), so a chunk (the vectors of
+// one thread in one step) without an element that reaches it cannot hold a result.  The bound is
+// taken anew after 1, 2, 4, 8, ... steps of the sweep: of N(0, 1) elements about 64 chunks of the
+// first step reach it at K = 64, and as many of each doubling, some 330 of a row of 151936.  The
+// chunks that also reach the last bound (about 64) are read again, and their elements that reach
+// it (about 70) are ranked by counting.
 //
 // Rows that collect more than the buffers hold (thousands of ties at the K-th value, large
 // values that come last) are done again by radix selection on order-preserving keys.
@@ -170,7 +172,7 @@ struct TopkPart {  // what one CTA of a cluster hands to the first
 // CS CTAs per row (a cluster when CS > 1).  Dynamic shared memory: cap candidates, then
 // kSurvivors, then (CS > 1) the CTAs' lists.
 template <class E, int CS>
-__global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p, int cap) {
+__global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams p, int cap) {
   using S = typename E::storage;
   constexpr int VEC = E::kVec, T = kTopkThreads, U = kUnroll;
   extern __shared__ uint64_t topk_smem[];
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p, 
   __shared__ TopkPart parts[CS];
   __shared__ float sh_thr;
   __shared__ unsigned sh_n, sh_m;
-  uint64_t* cand = topk_smem;
+  uint64_t* cand = topk_smem;  // chunks: the largest element's key, and the first vector
   uint64_t* surv = topk_smem + cap;
   uint64_t* lists = surv + kSurvivors;
   if (CS > 1) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
@@ -199,17 +201,19 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p, 
   MaxRun rs;
   float2 sub = make_float2(-INFINITY, -INFINITY);
   auto take = [&](float x, int j) {
-    const unsigned at = atomicAdd(&sh_n, 1u);
-    if (at < static_cast<unsigned>(cap)) cand[at] = entry_of(key_of(x), j);
+    const unsigned at = atomicAdd(&sh_m, 1u);
+    if (at < kSurvivors) surv[at] = entry_of(key_of(x), j);
   };
-  auto scalar = [&](int j) {
-    const float x = E::load_scalar(row + j);
-    maxrun_scalar(rs, x, c);
-    sub.x = fmaxf(sub.x, x);
-    if (x > -INFINITY) take(x, j);
-  };
-  if (rank == 0 && tid < sp.head) scalar(tid);
-  if (rank == CS - 1 && tid < sp.tail) scalar(sp.head + sp.nvec * VEC + tid);
+  // the scalar head and tail: at most one element per thread, kept for the end
+  float edge = -INFINITY;
+  int edge_j = -1;
+  if (rank == 0 && tid < sp.head) edge_j = tid;
+  if (rank == CS - 1 && tid >= T - sp.tail) edge_j = V - T + tid;
+  if (edge_j >= 0) {
+    edge = E::load_scalar(row + edge_j);
+    maxrun_scalar(rs, edge, c);
+    sub.x = fmaxf(sub.x, edge);
+  }
 
   float thr = -INFINITY;
   auto bound = [&]() {  // a new bound from the maxima so far
@@ -224,15 +228,8 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p, 
     thr = sh_thr;
   };
   const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
-  const uint32_t pad = sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
   int step = 0, next = 1;
-  for (int i0 = v0; i0 < v1; i0 += U * T) {
-    uint4 v[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int i = i0 + k * T + tid;
-      v[k] = i < v1 ? ld_nc_v4(vb + i) : make_uint4(pad, pad, pad, pad);
-    }
+  auto fold = [&](const uint4 (&v)[U], int i) {
     const float2 pm = maxrun_vectors<E>(rs, v, c);
     sub.x = fmaxf(sub.x, pm.x);
     sub.y = fmaxf(sub.y, pm.y);
@@ -242,32 +239,44 @@ __global__ void __launch_bounds__(kTopkThreads) topk_kernel(const TopkParams p, 
     }
     const float m = fmaxf(pm.x, pm.y);
     if (m >= thr && m > -INFINITY) {
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const uint4 one[1] = {v[k]};
-        const float2 mk = pair_max(one, static_cast<E*>(nullptr));
-        if (fmaxf(mk.x, mk.y) < thr) continue;
-        float f[VEC];
-        E::unpack(v[k], f);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q)
-          if (f[q] >= thr && f[q] > -INFINITY) take(f[q], sp.head + (i0 + k * T + tid) * VEC + q);
-      }
+      const unsigned at = atomicAdd(&sh_n, 1u);
+      if (at < static_cast<unsigned>(cap)) cand[at] = static_cast<uint64_t>(key_of(m)) << 32 | static_cast<uint32_t>(i);
     }
+  };
+  int i0 = v0;
+  for (; i0 + U * T <= v1; i0 += U * T) {
+    uint4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) v[k] = ld_nc_v4(vb + i0 + k * T + tid);
+    fold(v, i0 + tid);
+  }
+  if (i0 < v1) {
+    const uint32_t pad = sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    uint4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      v[k] = make_uint4(pad, pad, pad, pad);
+      if (i0 + k * T + tid < v1) v[k] = ld_nc_v4(vb + i0 + k * T + tid);
+    }
+    fold(v, i0 + tid);
   }
   if (step * 2 != next) bound();  // elements since the last bound
   MaxStat st = maxstat_block<T>(rs.stat(), c);
   __syncthreads();
 
-  // the candidates that pass the last bound
+  // the elements of the noted chunks that reach the last bound: four threads to a chunk
   const unsigned n = sh_n;
-  const uint64_t least = entry_of(key_of(thr), 0x7FFFFFFF);
-  for (unsigned i = tid; i < min(n, static_cast<unsigned>(cap)); i += T) {
-    const uint64_t e = cand[i];
-    if (e >= least) {
-      const unsigned at = atomicAdd(&sh_m, 1u);
-      if (at < kSurvivors) surv[at] = e;
-    }
+  const uint32_t least = key_of(thr);
+  if (edge > -INFINITY && edge >= thr) take(edge, edge_j);
+  for (unsigned q = tid; q < U * min(n, static_cast<unsigned>(cap)); q += T) {
+    const uint64_t e = cand[q / U];
+    const int i = static_cast<int>(static_cast<uint32_t>(e)) + static_cast<int>(q % U) * T;
+    if (static_cast<uint32_t>(e >> 32) < least || i >= v1) continue;
+    float f[VEC];
+    E::unpack(ld_nc_v4(vb + i), f);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (f[k] >= thr && f[k] > -INFINITY) take(f[k], sp.head + i * VEC + k);
   }
   __syncthreads();
   int m = static_cast<int>(sh_m);
