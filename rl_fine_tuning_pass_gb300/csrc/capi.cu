@@ -637,6 +637,7 @@ grpo_status check_rules(const grpo_logit_rules* q, const grpo_rows* x) {
   if (q->N < 0 || q->M < 0 || q->tokens_stride < 0 || q->allowed_stride_b < 0 || q->allowed_stride_l < 0)
     return GRPO_ERR_INVALID_ARG;
   if (q->N > grpo::kRuleMaxTokens || q->M > grpo::kRuleMaxBias) return GRPO_ERR_UNSUPPORTED;
+  if (static_cast<long double>(x->B) * x->L * ((x->V + 4095) / 4096) > kMaxRows) return GRPO_ERR_UNSUPPORTED;
   if (q->N > 0 && !ok_i64(q->tokens)) return GRPO_ERR_INVALID_ARG;
   if (q->M > 0 && (!ok_i64(q->bias_ids) || !ok_f32(q->bias))) return GRPO_ERR_INVALID_ARG;
   if (!aligned(q->hist_len, 4) || !aligned(q->prompt_len, 4) || !aligned(q->repetition, 4) ||

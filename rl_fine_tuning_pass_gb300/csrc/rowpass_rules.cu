@@ -6,17 +6,27 @@
 //   y_j += bias_j;   y_j = -inf where the mask forbids j
 //   dx_j = dy_j (s_j ? (x_j > 0 ? 1 / rho : rho) : 1),  0 where forbidden
 //
-// A CTA owns one tile of columns of a row: it counts the history into one 32-bit word per
-// column in shared memory (logits_ops.h), then streams the tile.  Values are formed in fp32
-// from the whole count and rounded once.
+// A CTA takes one tile of columns (1024 vectors) of a run of rows of one sequence.  The history of
+// the run's first row is counted into one 32-bit word per column in shared memory (logits_ops.h);
+// from row to row only the tokens that have come in are added (a row whose history is shorter
+// than the one before starts anew), so the history is read once per run and tile, not once per
+// row.  A bitmap tells which columns have a word: a vector without one is copied as it is.  The
+// gradient needs only which columns occur, so its bitmap is all that it keeps.
+//
+// The pass is bound by HBM (read and write every logit once).  The vectors of the next row are
+// loaded before the current ones are worked on; vectors that the mask forbids whole are not read.
+// Values are formed in fp32 from the whole count and rounded once.
 #include "logits_ops.h"
 #include "rowpass_common.cuh"
 
 namespace grpo {
 namespace {
 
-constexpr int kTileCols = 16384;  // 64 KB of words per CTA
 constexpr int kRulesThreads = 256;
+constexpr int kTileVecs = 1024;  // vectors of a row per CTA, 4 per thread
+constexpr int kPer = kTileVecs / kRulesThreads;
+constexpr int kMaxRun = 32;      // rows per CTA
+constexpr int kWindow = 256;     // tokens past the first row's history that are held ready
 
 struct SeqRules {
   float rho, freq, pres;
@@ -35,12 +45,11 @@ __device__ __forceinline__ float apply_rules(const SeqRules& q, float x, uint32_
   return x;
 }
 
-// Bits [j, j + n) of the row's mask, n <= 8.
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t* m, int j, int words) {
+// Bits j, j + 1, ... of a bitmap of `words` words (at least 25 of them, zeros past its end).
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* m, int j, int words) {
   const int w = j >> 5;
-  const uint32_t lo = __ldg(m + w);
-  const uint32_t hi = w + 1 < words ? __ldg(m + w + 1) : 0u;
-  return __funnelshift_r(lo, hi, j & 31);
+  const uint32_t hi = w + 1 < words ? m[w + 1] : 0u;
+  return __funnelshift_r(m[w], hi, j & 31);
 }
 
 template <class E>
@@ -52,150 +61,267 @@ __device__ __forceinline__ uint4 load_any(const typename E::storage* body, int i
   return E::pack(f, 0u);
 }
 
-template <class E, bool BWD>
-__global__ void __launch_bounds__(kRulesThreads) rules_kernel(const RulesParams p, int tiles, int tile_vecs,
-                                                              bool same_phase, bool in_place) {
-  extern __shared__ uint32_t words[];
-  wait_for_previous_grids();
-  constexpr int VEC = E::kVec;
+// Grid: tiles x runs, tiles innermost.  run: rows per CTA, runs: runs per sequence.
+// INPLACE: the output is the input, so only vectors that change are read and written.
+template <class E, bool BWD, bool INPLACE>
+__global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesParams p, int tiles, int run, int runs,
+                                                                 bool same_phase) {
+  constexpr int VEC = E::kVec, W = kTileVecs * VEC, COLS = W + VEC;  // a tile's last vector may reach past it
+  constexpr int MAPW = (COLS + 31) / 32 + 1;
   using S = typename E::storage;
+  extern __shared__ uint4 rules_smem[];  // words, one per column (forward)
+  __shared__ uint32_t touched[MAPW];
+  __shared__ int sh_len[kMaxRun];
+  __shared__ int window[kWindow];
+  uint32_t* words = reinterpret_cast<uint32_t*>(rules_smem);
+  wait_for_previous_grids();
   const int tid = threadIdx.x;
   const int tile = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles));
-  const int64_t r = blockIdx.x / static_cast<unsigned>(tiles);
-  const int64_t b = r / p.x.L, l = r - b * p.x.L;
-  const int V = p.x.V;
-  S* out = static_cast<S*>(p.out.ptr) + b * p.out.sb + l * p.out.sl;
-  const S* x = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
-  const S* src = BWD ? static_cast<const S*>(p.dy.ptr) + b * p.dy.sb + l * p.dy.sl : x;
-  const RowSplit sp = split_row<E>(out, V);
-  const int last = sp.nvec > 0 ? (sp.nvec - 1) / tile_vecs : 0;  // the tile that takes the row's tail
-  if (tile > last) return;
-  const int v0 = tile * tile_vecs;
-  const int v1 = min(sp.nvec, v0 + tile_vecs);
-  // columns [c0, c1) of this tile; word of column j: words[j - base]
-  const int c0 = tile == 0 ? 0 : sp.head + v0 * VEC;
-  const int c1 = tile == last ? V : sp.head + v1 * VEC;
-  const int base = sp.head + v0 * VEC - VEC;
+  const int64_t seq_run = blockIdx.x / static_cast<unsigned>(tiles);
+  const int64_t b = seq_run / runs;
+  const int64_t l0 = (seq_run - b * runs) * run;
+  const int nrows = static_cast<int>(min(static_cast<int64_t>(run), p.x.L - l0));
+  const int V = p.x.V, c0 = tile * W;
 
-  const bool counted = p.tokens != nullptr;
-  const bool used = counted || p.M > 0;
+  const bool counted = p.tokens != nullptr && (!BWD || p.repetition != nullptr);
+  const bool biased = !BWD && p.M > 0;
+  const bool used = counted || biased;
   SeqRules q;
   q.has_rep = counted && p.repetition != nullptr;
   q.rho = q.has_rep ? p.repetition[b] : 1.f;
   q.freq = counted && p.frequency ? p.frequency[b] : 0.f;
   q.pres = counted && p.presence ? p.presence[b] : 0.f;
   q.bias = p.bias + b * p.M;
+  const int64_t* tk = p.tokens + b * p.tokens_stride;
+  const int N = static_cast<int>(p.N);
+  const int np = !BWD && counted && p.prompt_len ? max(0, p.prompt_len[b]) : 0;
+  const int mwords = (V + 31) >> 5;
 
-  if (used) {
-    for (int i = tid; i < tile_vecs * VEC + 2 * VEC; i += kRulesThreads) words[i] = 0u;
+  auto bad_index = [&]() {
+    if (p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
+  };
+  auto add_token = [&](int col, int i) {  // column col of the tile, place i of the history
+    if (!BWD) {
+      if (i < np) atomicOr(&words[col], kRulePrompt);
+      else atomicAdd(&words[col], 1u);
+    }
+    atomicOr(&touched[col >> 5], 1u << (col & 31));
+  };
+  // the tile's column of a token, or -1
+  auto col_of = [&](int64_t id) {
+    if (id >= V) bad_index();
+    const int64_t col = id - c0;
+    return id >= 0 && id < V && col >= 0 && col < COLS ? static_cast<int>(col) : -1;
+  };
+  int held = 0;  // the words hold the history's first `held` tokens; the window what follows `win`
+  int win = 0;
+  auto rebuild = [&](int n) {  // count the first n tokens
     __syncthreads();
-    if (p.M > 0) {
-      const int64_t* ids = p.bias_ids + b * p.M;
+    if (!BWD)
+      for (int i = tid; i < (COLS + 3) / 4; i += kRulesThreads) rules_smem[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < MAPW; i += kRulesThreads) touched[i] = 0u;
+    __syncthreads();
+    if (biased) {
       for (int m = tid; m < p.M; m += kRulesThreads) {
-        const int64_t id = ids[m];
-        if (id >= V && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
+        const int col = col_of(p.bias_ids[b * p.M + m]);
+        if (col < 0) continue;
         // a column listed twice: the last entry counts
-        if (id >= c0 && id < c1) atomicMax(&words[id - base], static_cast<uint32_t>(m + 1) << kRuleBiasShift);
+        atomicMax(&words[col], static_cast<uint32_t>(m + 1) << kRuleBiasShift);
+        atomicOr(&touched[col >> 5], 1u << (col & 31));
       }
       __syncthreads();
     }
     if (counted) {
-      const int64_t* tk = p.tokens + b * p.tokens_stride;
-      int64_t n = p.hist_len ? p.hist_len[r] : p.N;
-      if (n < 0 || n > p.N) {
-        if (tid == 0 && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
-        n = n < 0 ? 0 : p.N;
+      int i = tid;
+      for (; i + 3 * kRulesThreads < n; i += 4 * kRulesThreads) {
+        int64_t id[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) id[k] = tk[i + k * kRulesThreads];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = col_of(id[k]);
+          if (col >= 0) add_token(col, i + k * kRulesThreads);
+        }
       }
-      const int64_t np = p.prompt_len ? p.prompt_len[b] : 0;
-      for (int64_t i = tid; i < n; i += kRulesThreads) {
-        const int64_t id = tk[i];
-        if (id >= V && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
-        if (id < c0 || id >= c1) continue;
-        if (i < np) atomicOr(&words[id - base], kRulePrompt);
-        else atomicAdd(&words[id - base], 1u);
+      for (; i < n; i += kRulesThreads) {
+        const int col = col_of(tk[i]);
+        if (col >= 0) add_token(col, i);
       }
-      __syncthreads();
+      if (nrows > 1 && tid < kWindow && n + tid < N) {
+        const int64_t id = tk[n + tid];
+        const int64_t col = id - c0;
+        window[tid] = id >= V ? -2 : (id >= 0 && col >= 0 && col < COLS ? static_cast<int>(col) : -1);
+      }
     }
+    held = win = n;
+    __syncthreads();
+  };
+
+  if (counted) {
+    for (int i = tid; i < nrows; i += kRulesThreads) {
+      int n = p.hist_len ? p.hist_len[b * p.x.L + l0 + i] : N;
+      if (n < 0 || n > N) {
+        bad_index();
+        n = n < 0 ? 0 : N;
+      }
+      sh_len[i] = n;
+    }
+    __syncthreads();
   }
 
-  const uint32_t* m = p.allowed ? p.allowed + b * p.allowed_sb + l * p.allowed_sl : nullptr;
-  const int mwords = (V + 31) >> 5;
-  auto scalar = [&](int j) {
-    const uint32_t w = used ? words[j - base] : 0u;
-    const bool ok = m == nullptr || (mask_bits(m, j, mwords) & 1u) != 0;
-    float v;
-    if (BWD) {
-      v = 0.f;
-      if (ok) {
-        v = E::load_scalar_coherent(src + j);
-        if (q.has_rep && in_history(w)) v = E::load_scalar_coherent(x + j) > 0.f ? __fdiv_rn(v, q.rho) : v * q.rho;
-      }
-    } else {
-      v = ok ? apply_rules(q, E::load_scalar_coherent(x + j), w) : -INFINITY;
-    }
-    E::store_scalar(out + j, v);
+  // the row's part in this tile: vectors [i0, i1), 1024 at most
+  struct Part {
+    const S* src;
+    const S* x;
+    S* out;
+    const uint32_t* m;
+    RowSplit sp;
+    int i0, i1;
   };
-  if (tile == 0 && tid < sp.head) scalar(tid);
-  if (tile == last && tid < sp.tail) scalar(sp.head + sp.nvec * VEC + tid);
-
-  uint4* ob = reinterpret_cast<uint4*>(out + sp.head);
-  const S* sb = src + sp.head;
+  auto part_of = [&](int rr) {
+    const int64_t l = l0 + rr;
+    Part t;
+    t.out = static_cast<S*>(p.out.ptr) + b * p.out.sb + l * p.out.sl;
+    t.x = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
+    t.src = BWD ? static_cast<const S*>(p.dy.ptr) + b * p.dy.sb + l * p.dy.sl : t.x;
+    t.m = p.allowed ? p.allowed + b * p.allowed_sb + l * p.allowed_sl : nullptr;
+    t.sp = split_row<E>(t.out, V);
+    // a vector belongs to the tile of its first column
+    t.i0 = c0 <= t.sp.head ? 0 : (c0 - t.sp.head + VEC - 1) / VEC;
+    t.i1 = min(t.sp.nvec, (c0 + W - t.sp.head + VEC - 1) / VEC);
+    return t;
+  };
   constexpr uint32_t kAll = (1u << VEC) - 1u;
-  for (int i = v0 + tid; i < v1; i += kRulesThreads) {
-    const int j = sp.head + i * VEC;
-    uint32_t w[VEC];
-    uint32_t any = 0u;
-    if (used) {
+  auto load = [&](const Part& t, uint4 (&v)[kPer], uint32_t (&ok)[kPer]) {
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) any |= w[k] = words[j - base + k];
+    for (int k = 0; k < kPer; ++k) {
+      const int i = t.i0 + tid + k * kRulesThreads;
+      ok[k] = i < t.i1 && t.m ? bits_at(t.m, t.sp.head + i * VEC, mwords) & kAll : kAll;
     }
-    const uint32_t ok = m ? mask_bits(m, j, mwords) & kAll : kAll;
-    if (in_place && any == 0u && ok == kAll) continue;  // the output is the input already
-    float f[VEC];
-    if (ok != 0u) E::unpack(load_any<E>(sb, i, same_phase), f);
-    if (any != 0u) {
+    if (INPLACE) return;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        if (BWD) {
-          if (q.has_rep && in_history(w[k]))
-            f[k] = E::load_scalar_coherent(x + j + k) > 0.f ? __fdiv_rn(f[k], q.rho) : f[k] * q.rho;
-        } else {
-          f[k] = apply_rules(q, f[k], w[k]);
+    for (int k = 0; k < kPer; ++k) {
+      const int i = t.i0 + tid + k * kRulesThreads;
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < t.i1 && ok[k] != 0u) v[k] = load_any<E>(t.src + t.sp.head, i, same_phase);
+    }
+  };
+
+  uint4 v[kPer];
+  uint32_t ok[kPer];
+  Part cur = part_of(0);
+  load(cur, v, ok);
+  if (used) rebuild(counted ? sh_len[0] : 0);
+  for (int rr = 0; rr < nrows; ++rr) {
+    if (counted && rr > 0) {
+      const int n = sh_len[rr];
+      if (n < held || n > win + kWindow) {
+        rebuild(n);
+      } else {
+        for (; held < n; ++held) {  // the same in every thread; a token of this tile is seldom
+          const int col = window[held - win];
+          if (col == -2) bad_index();
+          if (col < 0) continue;
+          __syncthreads();
+          if (tid == 0) add_token(col, held);
+          __syncthreads();
         }
       }
     }
+    uint4 nv[kPer];
+    uint32_t nok[kPer];
+    Part next = cur;
+    if (rr + 1 < nrows) {
+      next = part_of(rr + 1);
+      load(next, nv, nok);
+    }
+
+    auto scalar = [&](int j) {
+      const uint32_t w = used && (touched[(j - c0) >> 5] >> ((j - c0) & 31) & 1u) ? (BWD ? 1u : words[j - c0]) : 0u;
+      float f = BWD ? 0.f : -INFINITY;
+      if (cur.m == nullptr || (bits_at(cur.m, j, mwords) & 1u) != 0) {
+        f = E::load_scalar_coherent(cur.src + j);
+        if (!BWD) f = apply_rules(q, f, w);
+        else if (w != 0u) f = E::load_scalar_coherent(cur.x + j) > 0.f ? __fdiv_rn(f, q.rho) : f * q.rho;
+      }
+      E::store_scalar(cur.out + j, f);
+    };
+    if (tid < cur.sp.head && tid >= c0 && tid < c0 + W) scalar(tid);
+    const int jt = cur.sp.head + cur.sp.nvec * VEC + tid;
+    if (tid < cur.sp.tail && jt >= c0 && jt < c0 + W) scalar(jt);
+
+    uint4* ob = reinterpret_cast<uint4*>(cur.out + cur.sp.head);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k)
-      if (!(ok >> k & 1u)) f[k] = BWD ? 0.f : -INFINITY;
-    st_v4_evict_first(ob + i, E::pack(f, 0u));
+    for (int k = 0; k < kPer; ++k) {
+      const int i = cur.i0 + tid + k * kRulesThreads;
+      if (i >= cur.i1) continue;
+      const int j = cur.sp.head + i * VEC;
+      const uint32_t any = used ? bits_at(touched, j - c0, MAPW) & kAll : 0u;
+      if (INPLACE) {
+        if (any == 0u && ok[k] == kAll) continue;  // the output is the input already
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (ok[k] != 0u) v[k] = load_any<E>(cur.src + cur.sp.head, i, same_phase);
+      }
+      if (any != 0u || ok[k] != kAll) {
+        float f[VEC];
+        E::unpack(v[k], f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          if (any >> e & 1u) {
+            if (!BWD) f[e] = apply_rules(q, f[e], words[j - c0 + e]);
+            else f[e] = E::load_scalar_coherent(cur.x + j + e) > 0.f ? __fdiv_rn(f[e], q.rho) : f[e] * q.rho;
+          }
+          if (!(ok[k] >> e & 1u)) f[e] = BWD ? 0.f : -INFINITY;
+        }
+        v[k] = E::pack(f, 0u);
+      }
+      st_v4_evict_first(ob + i, v[k]);
+    }
+    cur = next;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      v[k] = nv[k];
+      ok[k] = nok[k];
+    }
   }
 }
 
-template <class E, bool BWD>
-cudaError_t launch_e(bool same_phase, bool in_place, const RulesParams& p, int64_t rows, cudaStream_t s) {
-  constexpr int VEC = E::kVec;
-  const int nvec = (p.x.V + VEC - 1) / VEC;
-  const int tile_vecs = kTileCols / VEC;
-  const int tiles = (nvec + tile_vecs - 1) / tile_vecs;
-  const bool used = p.tokens != nullptr || p.M > 0;
-  const size_t smem = used ? (static_cast<size_t>(kTileCols) + 2 * VEC) * 4 : 0;
-  const cudaError_t e = cudaFuncSetAttribute(rules_kernel<E, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (kTileCols + 2 * VEC) * 4);
+template <class E, bool BWD, bool INPLACE>
+cudaError_t launch_e(bool same_phase, const RulesParams& p, int64_t rows, int sms, cudaStream_t s) {
+  constexpr int W = kTileVecs * E::kVec, COLS = W + E::kVec;
+  const int tiles = (p.x.V + W - 1) / W;
+  // rows per CTA: long runs count the history seldom, but leave 6 CTAs or more for each place
+  const int64_t places = 4LL * sms;
+  int64_t run = rows * tiles / (6 * places);
+  run = run < 1 ? 1 : (run > kMaxRun ? kMaxRun : run);
+  if (run > p.x.L) run = p.x.L;
+  const int64_t runs = (p.x.L + run - 1) / run;
+  const bool used = !BWD && (p.tokens != nullptr || p.M > 0);
+  const int most = (COLS + 3) / 4 * 16;
+  const cudaError_t e = cudaFuncSetAttribute(rules_kernel<E, BWD, INPLACE>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
-  return launch_after_previous_smem(rules_kernel<E, BWD>, dim3(static_cast<unsigned>(rows * tiles)),
-                                    dim3(kRulesThreads), smem, s, p, tiles, tile_vecs, same_phase, in_place);
+  const int64_t grid = rows / p.x.L * runs * tiles;
+  return launch_after_previous_smem(rules_kernel<E, BWD, INPLACE>, dim3(static_cast<unsigned>(grid)),
+                                    dim3(kRulesThreads), used ? most : 0, s, p, tiles, static_cast<int>(run),
+                                    static_cast<int>(runs), same_phase);
+}
+
+template <class E>
+cudaError_t launch_d(bool bwd, bool same_phase, bool in_place, const RulesParams& p, int64_t rows, int sms,
+                     cudaStream_t s) {
+  if (bwd) return in_place ? launch_e<E, true, true>(same_phase, p, rows, sms, s)
+                           : launch_e<E, true, false>(same_phase, p, rows, sms, s);
+  return in_place ? launch_e<E, false, true>(same_phase, p, rows, sms, s)
+                  : launch_e<E, false, false>(same_phase, p, rows, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rules(int dtype, bool bwd, bool same_phase, bool in_place, const RulesParams& p, int64_t rows,
                          int sms, cudaStream_t stream) {
-  (void)sms;
-  if (dtype == 1)
-    return bwd ? launch_e<BF16, true>(same_phase, in_place, p, rows, stream)
-               : launch_e<BF16, false>(same_phase, in_place, p, rows, stream);
-  return bwd ? launch_e<F32, true>(same_phase, in_place, p, rows, stream)
-             : launch_e<F32, false>(same_phase, in_place, p, rows, stream);
+  return dtype == 1 ? launch_d<BF16>(bwd, same_phase, in_place, p, rows, sms, stream)
+                    : launch_d<F32>(bwd, same_phase, in_place, p, rows, sms, stream);
 }
 
 }  // namespace grpo
