@@ -13,9 +13,11 @@
 // row.  A bitmap tells which columns have a word: a vector without one is copied as it is.  The
 // gradient needs only which columns occur, so its bitmap is all that it keeps.
 //
-// The pass is bound by HBM (read and write every logit once).  The vectors of the next row are
-// loaded before the current ones are worked on; vectors that the mask forbids whole are not read.
-// Values are formed in fp32 from the whole count and rounded once.
+// The pass is bound by HBM (read and write every logit once): five CTAs per SM with four vectors in
+// flight per thread cover its latency; vectors that the mask forbids whole are not read.  What
+// touched columns need stands outside the stream in functions of its own: inlined, it filled the
+// instruction cache and the stream waited for instructions.  Values are formed in fp32 from the
+// whole count and rounded once.
 #include "logits_ops.h"
 #include "rowpass_common.cuh"
 
@@ -36,13 +38,51 @@ struct SeqRules {
 
 __device__ __forceinline__ bool in_history(uint32_t w) { return (w & ((1u << kRuleBiasShift) - 1)) != 0; }
 
-__device__ __forceinline__ float apply_rules(const SeqRules& q, float x, uint32_t w) {
+__device__ __noinline__ float apply_rules(const SeqRules q, float x, uint32_t w) {
   if (q.has_rep && in_history(w)) x = x > 0.f ? __fdiv_rn(x, q.rho) : x * q.rho;
   const uint32_t n = w & (kRulePrompt - 1);
   if (n != 0) x = fmaf(-q.freq, static_cast<float>(n), x) - q.pres;
   const uint32_t at = w >> kRuleBiasShift;
   if (at != 0) x += q.bias[at - 1];
   return x;
+}
+
+__device__ __noinline__ float apply_slope(float rho, float dy, float x) { return x > 0.f ? __fdiv_rn(dy, rho) : dy * rho; }
+
+// Element e of a vector, read and replaced, without indexing registers.
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
+  return k == 0 ? v.x : (k == 1 ? v.y : (k == 2 ? v.z : v.w));
+}
+__device__ __forceinline__ void set_word(uint4& v, int k, uint32_t w) {
+  v.x = k == 0 ? w : v.x;
+  v.y = k == 1 ? w : v.y;
+  v.z = k == 2 ? w : v.z;
+  v.w = k == 3 ? w : v.w;
+}
+__device__ __forceinline__ float get_elem(const uint4& v, int e, BF16*) {
+  const uint32_t w = word_of(v, e >> 1);
+  return e & 1 ? BF16::hi(w) : BF16::lo(w);
+}
+__device__ __forceinline__ float get_elem(const uint4& v, int e, F32*) { return __uint_as_float(word_of(v, e)); }
+__device__ __forceinline__ void set_elem(uint4& v, int e, float f, BF16*) {
+  const uint32_t h = BF16::pack2(f, 0.f) & 0xFFFFu, w = word_of(v, e >> 1);
+  set_word(v, e >> 1, e & 1 ? (w & 0xFFFFu) | h << 16 : (w & 0xFFFF0000u) | h);
+}
+__device__ __forceinline__ void set_elem(uint4& v, int e, float f, F32*) { set_word(v, e, __float_as_uint(f)); }
+
+// `fill` (a pair of equal elements, or one fp32) where ok's bit is 0.
+__device__ __forceinline__ void forbid(uint4& v, uint32_t ok, uint32_t fill, BF16*) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t keep = (ok >> (2 * k) & 1u) * 0xFFFFu | (ok >> (2 * k + 1) & 1u) * 0xFFFF0000u;
+    w[k] = (w[k] & keep) | (fill & ~keep);
+  }
+}
+__device__ __forceinline__ void forbid(uint4& v, uint32_t ok, uint32_t fill, F32*) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = ok >> k & 1u ? w[k] : fill;
 }
 
 // Bits j, j + 1, ... of a bitmap of `words` words (at least 25 of them, zeros past its end).
@@ -64,7 +104,7 @@ __device__ __forceinline__ uint4 load_any(const typename E::storage* body, int i
 // Grid: tiles x runs, tiles innermost.  run: rows per CTA, runs: runs per sequence.
 // INPLACE: the output is the input, so only vectors that change are read and written.
 template <class E, bool BWD, bool INPLACE>
-__global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesParams p, int tiles, int run, int runs,
+__global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesParams p, int tiles, int run, int runs,
                                                                  bool same_phase) {
   constexpr int VEC = E::kVec, W = kTileVecs * VEC, COLS = W + VEC;  // a tile's last vector may reach past it
   constexpr int MAPW = (COLS + 31) / 32 + 1;
@@ -192,30 +232,45 @@ __global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesPara
     return t;
   };
   constexpr uint32_t kAll = (1u << VEC) - 1u;
-  auto load = [&](const Part& t, uint4 (&v)[kPer], uint32_t (&ok)[kPer]) {
+  // the vectors and which of their columns are allowed (a byte each)
+  auto load = [&](const Part& t, uint4 (&v)[kPer]) {
+    uint32_t allowed = 0xFFFFFFFFu;
+    if (t.m != nullptr) {
+      allowed = 0u;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int i = t.i0 + tid + k * kRulesThreads;
-      ok[k] = i < t.i1 && t.m ? bits_at(t.m, t.sp.head + i * VEC, mwords) & kAll : kAll;
+      for (int k = 0; k < kPer; ++k) {
+        const int i = t.i0 + tid + k * kRulesThreads;
+        if (i < t.i1) allowed |= (bits_at(t.m, t.sp.head + i * VEC, mwords) & kAll) << (8 * k);
+      }
     }
-    if (INPLACE) return;
+    if (INPLACE) return allowed;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int i = t.i0 + tid + k * kRulesThreads;
       v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < t.i1 && ok[k] != 0u) v[k] = load_any<E>(t.src + t.sp.head, i, same_phase);
+      if (i < t.i1 && (allowed >> (8 * k) & kAll) != 0u) v[k] = load_any<E>(t.src + t.sp.head, i, same_phase);
+    }
+    return allowed;
+  };
+
+  // a vector's touched columns, one after the other
+  auto touch = [&](const Part& t, uint4& v, int j, uint32_t any) {
+    while (any != 0u) {
+      const int e = __ffs(any) - 1;
+      any &= any - 1u;
+      float f = get_elem(v, e, static_cast<E*>(nullptr));
+      f = BWD ? apply_slope(q.rho, f, E::load_scalar_coherent(t.x + j + e)) : apply_rules(q, f, words[j - c0 + e]);
+      set_elem(v, e, f, static_cast<E*>(nullptr));
     }
   };
 
-  uint4 v[kPer];
-  uint32_t ok[kPer];
-  Part cur = part_of(0);
-  load(cur, v, ok);
-  if (used) rebuild(counted ? sh_len[0] : 0);
   for (int rr = 0; rr < nrows; ++rr) {
-    if (counted && rr > 0) {
-      const int n = sh_len[rr];
-      if (n < held || n > win + kWindow) {
+    const Part cur = part_of(rr);
+    uint4 v[kPer];
+    const uint32_t allowed = load(cur, v);
+    if (used) {
+      const int n = counted ? sh_len[rr] : 0;
+      if (rr == 0 || n < held || n > win + kWindow) {
         rebuild(n);
       } else {
         for (; held < n; ++held) {  // the same in every thread; a token of this tile is seldom
@@ -228,27 +283,20 @@ __global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesPara
         }
       }
     }
-    uint4 nv[kPer];
-    uint32_t nok[kPer];
-    Part next = cur;
-    if (rr + 1 < nrows) {
-      next = part_of(rr + 1);
-      load(next, nv, nok);
-    }
 
     auto scalar = [&](int j) {
-      const uint32_t w = used && (touched[(j - c0) >> 5] >> ((j - c0) & 31) & 1u) ? (BWD ? 1u : words[j - c0]) : 0u;
+      const bool hit = used && (touched[(j - c0) >> 5] >> ((j - c0) & 31) & 1u);
       float f = BWD ? 0.f : -INFINITY;
       if (cur.m == nullptr || (bits_at(cur.m, j, mwords) & 1u) != 0) {
         f = E::load_scalar_coherent(cur.src + j);
-        if (!BWD) f = apply_rules(q, f, w);
-        else if (w != 0u) f = E::load_scalar_coherent(cur.x + j) > 0.f ? __fdiv_rn(f, q.rho) : f * q.rho;
+        if (hit) f = BWD ? apply_slope(q.rho, f, E::load_scalar_coherent(cur.x + j)) : apply_rules(q, f, words[j - c0]);
       }
       E::store_scalar(cur.out + j, f);
     };
-    if (tid < cur.sp.head && tid >= c0 && tid < c0 + W) scalar(tid);
-    const int jt = cur.sp.head + cur.sp.nvec * VEC + tid;
-    if (tid < cur.sp.tail && jt >= c0 && jt < c0 + W) scalar(jt);
+    // the scalar head and tail, at most one element per thread
+    int edge = tid < cur.sp.head ? tid : -1;
+    if (tid >= kRulesThreads - cur.sp.tail) edge = V - kRulesThreads + tid;
+    if (edge >= c0 && edge < c0 + W) scalar(edge);
 
     uint4* ob = reinterpret_cast<uint4*>(cur.out + cur.sp.head);
 #pragma unroll
@@ -256,32 +304,17 @@ __global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesPara
       const int i = cur.i0 + tid + k * kRulesThreads;
       if (i >= cur.i1) continue;
       const int j = cur.sp.head + i * VEC;
-      const uint32_t any = used ? bits_at(touched, j - c0, MAPW) & kAll : 0u;
+      const uint32_t ok = allowed >> (8 * k) & kAll;
+      const uint32_t any = used ? bits_at(touched, j - c0, MAPW) & ok : 0u;
       if (INPLACE) {
-        if (any == 0u && ok[k] == kAll) continue;  // the output is the input already
+        if (any == 0u && ok == kAll) continue;  // the output is the input already
         v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (ok[k] != 0u) v[k] = load_any<E>(cur.src + cur.sp.head, i, same_phase);
+        if (ok != 0u) v[k] = load_any<E>(cur.src + cur.sp.head, i, same_phase);
       }
-      if (any != 0u || ok[k] != kAll) {
-        float f[VEC];
-        E::unpack(v[k], f);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          if (any >> e & 1u) {
-            if (!BWD) f[e] = apply_rules(q, f[e], words[j - c0 + e]);
-            else f[e] = E::load_scalar_coherent(cur.x + j + e) > 0.f ? __fdiv_rn(f[e], q.rho) : f[e] * q.rho;
-          }
-          if (!(ok[k] >> e & 1u)) f[e] = BWD ? 0.f : -INFINITY;
-        }
-        v[k] = E::pack(f, 0u);
-      }
+      if (any != 0u) touch(cur, v[k], j, any);
+      if (ok != kAll)
+        forbid(v[k], ok, BWD ? 0u : (sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u), static_cast<E*>(nullptr));
       st_v4_evict_first(ob + i, v[k]);
-    }
-    cur = next;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      v[k] = nv[k];
-      ok[k] = nok[k];
     }
   }
 }
@@ -291,7 +324,7 @@ cudaError_t launch_e(bool same_phase, const RulesParams& p, int64_t rows, int sm
   constexpr int W = kTileVecs * E::kVec, COLS = W + E::kVec;
   const int tiles = (p.x.V + W - 1) / W;
   // rows per CTA: long runs count the history seldom, but leave 6 CTAs or more for each place
-  const int64_t places = 4LL * sms;
+  const int64_t places = 5LL * sms;
   int64_t run = rows * tiles / (6 * places);
   run = run < 1 ? 1 : (run > kMaxRun ? kMaxRun : run);
   if (run > p.x.L) run = p.x.L;
