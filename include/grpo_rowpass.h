@@ -509,7 +509,7 @@ typedef struct {
  *            overlap).  It may alias logits exactly: then only what the rules change is read
  *            and written
  *   dout     [B, L, V] gradient of the processed logits, same dtype and shape, its own strides
- *   dlogits  [B, L, V] output like out; it may alias dout exactly, or logits exactly
+ *   dlogits  [B, L, V] output like out; it may alias dout exactly, and may not overlap logits
  * A token or bias id >= V sets GRPO_DEVERR_IDX_OUT_OF_RANGE and is skipped.  The history of a
  * row is read in full only for the first row of a run of rows whose hist_len does not fall.
  */

@@ -733,6 +733,7 @@ grpo_status process_logits_bwd(const grpo_rows* logits, const grpo_rows* dout, c
     return GRPO_ERR_INVALID_ARG;
   bool same_phase = false;
   if ((st = check_dlogits(logits, dlogits, &same_phase)) != GRPO_OK) return st;
+  if (rows_of(logits) > 0 && logits->ptr == dlogits->ptr) return GRPO_ERR_INVALID_ARG;  // the logits are read late
   if ((st = check_dlogits(dout, dlogits, &same_phase)) != GRPO_OK) return st;
   if (rules == nullptr) return GRPO_ERR_INVALID_ARG;
   if (rows_of(logits) == 0) return GRPO_OK;

@@ -10,14 +10,14 @@
 // the run's first row is counted into one 32-bit word per column in shared memory (logits_ops.h);
 // from row to row only the tokens that have come in are added (a row whose history is shorter
 // than the one before starts anew), so the history is read once per run and tile, not once per
-// row.  A bitmap tells which columns have a word: a vector without one is copied as it is.  The
-// gradient needs only which columns occur, so its bitmap is all that it keeps.
+// row.  The gradient needs only which columns occur, and keeps no words.
 //
-// The pass is bound by HBM (read and write every logit once): five CTAs per SM with four vectors in
-// flight per thread cover its latency; vectors that the mask forbids whole are not read.  What
-// touched columns need stands outside the stream in functions of its own: inlined, it filled the
-// instruction cache and the stream waited for instructions.  Values are formed in fp32 from the
-// whole count and rounded once.
+// The pass is bound by HBM (read and write every logit once), so the stream over a row is a copy
+// (with -inf or 0 where the mask forbids; vectors that it forbids whole are not read).  The touched
+// columns, listed as they are first met, are written over the copy, a thread to each: within the
+// stream nearly every warp met one, and its 32 lanes waited for it (1.24 ms against DUAL ms for
+// forward and backward at (4, 1024, 151936) bf16).  Values are formed in fp32 from the whole count
+// and rounded once.
 #include "logits_ops.h"
 #include "rowpass_common.cuh"
 
@@ -29,6 +29,7 @@ constexpr int kTileVecs = 1024;  // vectors of a row per CTA, 4 per thread
 constexpr int kPer = kTileVecs / kRulesThreads;
 constexpr int kMaxRun = 32;      // rows per CTA
 constexpr int kWindow = 256;     // tokens past the first row's history that are held ready
+constexpr int kListed = 2048;    // touched columns that are listed; with more, the bitmap is searched
 
 struct SeqRules {
   float rho, freq, pres;
@@ -38,7 +39,7 @@ struct SeqRules {
 
 __device__ __forceinline__ bool in_history(uint32_t w) { return (w & ((1u << kRuleBiasShift) - 1)) != 0; }
 
-__device__ __noinline__ float apply_rules(const SeqRules q, float x, uint32_t w) {
+__device__ __forceinline__ float apply_rules(const SeqRules& q, float x, uint32_t w) {
   if (q.has_rep && in_history(w)) x = x > 0.f ? __fdiv_rn(x, q.rho) : x * q.rho;
   const uint32_t n = w & (kRulePrompt - 1);
   if (n != 0) x = fmaf(-q.freq, static_cast<float>(n), x) - q.pres;
@@ -46,29 +47,6 @@ __device__ __noinline__ float apply_rules(const SeqRules q, float x, uint32_t w)
   if (at != 0) x += q.bias[at - 1];
   return x;
 }
-
-__device__ __noinline__ float apply_slope(float rho, float dy, float x) { return x > 0.f ? __fdiv_rn(dy, rho) : dy * rho; }
-
-// Element e of a vector, read and replaced, without indexing registers.
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
-  return k == 0 ? v.x : (k == 1 ? v.y : (k == 2 ? v.z : v.w));
-}
-__device__ __forceinline__ void set_word(uint4& v, int k, uint32_t w) {
-  v.x = k == 0 ? w : v.x;
-  v.y = k == 1 ? w : v.y;
-  v.z = k == 2 ? w : v.z;
-  v.w = k == 3 ? w : v.w;
-}
-__device__ __forceinline__ float get_elem(const uint4& v, int e, BF16*) {
-  const uint32_t w = word_of(v, e >> 1);
-  return e & 1 ? BF16::hi(w) : BF16::lo(w);
-}
-__device__ __forceinline__ float get_elem(const uint4& v, int e, F32*) { return __uint_as_float(word_of(v, e)); }
-__device__ __forceinline__ void set_elem(uint4& v, int e, float f, BF16*) {
-  const uint32_t h = BF16::pack2(f, 0.f) & 0xFFFFu, w = word_of(v, e >> 1);
-  set_word(v, e >> 1, e & 1 ? (w & 0xFFFFu) | h << 16 : (w & 0xFFFF0000u) | h);
-}
-__device__ __forceinline__ void set_elem(uint4& v, int e, float f, F32*) { set_word(v, e, __float_as_uint(f)); }
 
 // `fill` (a pair of equal elements, or one fp32) where ok's bit is 0.
 __device__ __forceinline__ void forbid(uint4& v, uint32_t ok, uint32_t fill, BF16*) {
@@ -102,15 +80,17 @@ __device__ __forceinline__ uint4 load_any(const typename E::storage* body, int i
 }
 
 // Grid: tiles x runs, tiles innermost.  run: rows per CTA, runs: runs per sequence.
-// INPLACE: the output is the input, so only vectors that change are read and written.
+// INPLACE: the output is the input, so only what changes is read and written.
 template <class E, bool BWD, bool INPLACE>
 __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesParams p, int tiles, int run, int runs,
                                                                  bool same_phase) {
   constexpr int VEC = E::kVec, W = kTileVecs * VEC, COLS = W + VEC;  // a tile's last vector may reach past it
-  constexpr int MAPW = (COLS + 31) / 32 + 1;
+  constexpr int MAPW = (COLS + 31) / 32;
   using S = typename E::storage;
   extern __shared__ uint4 rules_smem[];  // words, one per column (forward)
   __shared__ uint32_t touched[MAPW];
+  __shared__ uint16_t listed[kListed];
+  __shared__ int sh_touched;
   __shared__ int sh_len[kMaxRun];
   __shared__ int window[kWindow];
   uint32_t* words = reinterpret_cast<uint32_t*>(rules_smem);
@@ -140,18 +120,23 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
   auto bad_index = [&]() {
     if (p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
   };
+  auto touch = [&](int col) {
+    const uint32_t bit = 1u << (col & 31);
+    if (atomicOr(&touched[col >> 5], bit) & bit) return;
+    const int at = atomicAdd(&sh_touched, 1);
+    if (at < kListed) listed[at] = static_cast<uint16_t>(col);
+  };
   auto add_token = [&](int col, int i) {  // column col of the tile, place i of the history
     if (!BWD) {
       if (i < np) atomicOr(&words[col], kRulePrompt);
       else atomicAdd(&words[col], 1u);
     }
-    atomicOr(&touched[col >> 5], 1u << (col & 31));
+    touch(col);
   };
-  // the tile's column of a token, or -1
+  // the tile's column of a token, -1 where it has none, -2 past the vocabulary
   auto col_of = [&](int64_t id) {
-    if (id >= V) bad_index();
     const int64_t col = id - c0;
-    return id >= 0 && id < V && col >= 0 && col < COLS ? static_cast<int>(col) : -1;
+    return id >= V ? -2 : (id >= 0 && col >= 0 && col < COLS ? static_cast<int>(col) : -1);
   };
   int held = 0;  // the words hold the history's first `held` tokens; the window what follows `win`
   int win = 0;
@@ -160,38 +145,32 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
     if (!BWD)
       for (int i = tid; i < (COLS + 3) / 4; i += kRulesThreads) rules_smem[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < MAPW; i += kRulesThreads) touched[i] = 0u;
+    if (tid == 0) sh_touched = 0;
     __syncthreads();
     if (biased) {
       for (int m = tid; m < p.M; m += kRulesThreads) {
         const int col = col_of(p.bias_ids[b * p.M + m]);
+        if (col == -2) bad_index();
         if (col < 0) continue;
         // a column listed twice: the last entry counts
         atomicMax(&words[col], static_cast<uint32_t>(m + 1) << kRuleBiasShift);
-        atomicOr(&touched[col >> 5], 1u << (col & 31));
+        touch(col);
       }
       __syncthreads();
     }
     if (counted) {
-      int i = tid;
-      for (; i + 3 * kRulesThreads < n; i += 4 * kRulesThreads) {
+      for (int i0 = tid; i0 < n; i0 += 4 * kRulesThreads) {
         int64_t id[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) id[k] = tk[i + k * kRulesThreads];
+        for (int k = 0; k < 4; ++k) id[k] = i0 + k * kRulesThreads < n ? tk[i0 + k * kRulesThreads] : -1;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int col = col_of(id[k]);
-          if (col >= 0) add_token(col, i + k * kRulesThreads);
+          if (col == -2) bad_index();
+          if (col >= 0) add_token(col, i0 + k * kRulesThreads);
         }
       }
-      for (; i < n; i += kRulesThreads) {
-        const int col = col_of(tk[i]);
-        if (col >= 0) add_token(col, i);
-      }
-      if (nrows > 1 && tid < kWindow && n + tid < N) {
-        const int64_t id = tk[n + tid];
-        const int64_t col = id - c0;
-        window[tid] = id >= V ? -2 : (id >= 0 && col >= 0 && col < COLS ? static_cast<int>(col) : -1);
-      }
+      if (nrows > 1 && tid < kWindow && n + tid < N) window[tid] = col_of(tk[n + tid]);
     }
     held = win = n;
     __syncthreads();
@@ -209,65 +188,38 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
     __syncthreads();
   }
 
-  // the row's part in this tile: vectors [i0, i1), 1024 at most
-  struct Part {
-    const S* src;
-    const S* x;
-    S* out;
-    const uint32_t* m;
-    RowSplit sp;
-    int i0, i1;
-  };
-  auto part_of = [&](int rr) {
-    const int64_t l = l0 + rr;
-    Part t;
-    t.out = static_cast<S*>(p.out.ptr) + b * p.out.sb + l * p.out.sl;
-    t.x = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
-    t.src = BWD ? static_cast<const S*>(p.dy.ptr) + b * p.dy.sb + l * p.dy.sl : t.x;
-    t.m = p.allowed ? p.allowed + b * p.allowed_sb + l * p.allowed_sl : nullptr;
-    t.sp = split_row<E>(t.out, V);
-    // a vector belongs to the tile of its first column
-    t.i0 = c0 <= t.sp.head ? 0 : (c0 - t.sp.head + VEC - 1) / VEC;
-    t.i1 = min(t.sp.nvec, (c0 + W - t.sp.head + VEC - 1) / VEC);
-    return t;
-  };
   constexpr uint32_t kAll = (1u << VEC) - 1u;
-  // the vectors and which of their columns are allowed (a byte each)
-  auto load = [&](const Part& t, uint4 (&v)[kPer]) {
+  constexpr uint32_t kForbidden = BWD ? 0u : (sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u);  // 0 or -inf
+  for (int rr = 0; rr < nrows; ++rr) {
+    const int64_t l = l0 + rr;
+    S* out = static_cast<S*>(p.out.ptr) + b * p.out.sb + l * p.out.sl;
+    const S* src = BWD ? static_cast<const S*>(p.dy.ptr) + b * p.dy.sb + l * p.dy.sl
+                       : static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
+    const uint32_t* m = p.allowed ? p.allowed + b * p.allowed_sb + l * p.allowed_sl : nullptr;
+    const RowSplit sp = split_row<E>(out, V);
+    // the row's part in this tile: vectors [i0, i1), 1024 at most; a vector belongs to the tile of
+    // its first column
+    const int i0 = c0 <= sp.head ? 0 : (c0 - sp.head + VEC - 1) / VEC;
+    const int i1 = min(sp.nvec, (c0 + W - sp.head + VEC - 1) / VEC);
+
+    // the vectors, and which of their columns are allowed (a byte each)
     uint32_t allowed = 0xFFFFFFFFu;
-    if (t.m != nullptr) {
-      allowed = 0u;
+    if (m != nullptr) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        const int i = t.i0 + tid + k * kRulesThreads;
-        if (i < t.i1) allowed |= (bits_at(t.m, t.sp.head + i * VEC, mwords) & kAll) << (8 * k);
+        const int i = i0 + tid + k * kRulesThreads;
+        if (i < i1) allowed ^= (bits_at(m, sp.head + i * VEC, mwords) & kAll ^ kAll) << (8 * k);
       }
     }
-    if (INPLACE) return allowed;
+    auto full = [&](int k) { return (allowed >> (8 * k) & kAll) == kAll; };
+    auto none = [&](int k) { return (allowed >> (8 * k) & kAll) == 0u; };
+    uint4 v[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int i = t.i0 + tid + k * kRulesThreads;
-      v[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < t.i1 && (allowed >> (8 * k) & kAll) != 0u) v[k] = load_any<E>(t.src + t.sp.head, i, same_phase);
+      const int i = i0 + tid + k * kRulesThreads;
+      if (i < i1 && !none(k) && !(INPLACE && full(k))) v[k] = load_any<E>(src + sp.head, i, same_phase);
     }
-    return allowed;
-  };
 
-  // a vector's touched columns, one after the other
-  auto touch = [&](const Part& t, uint4& v, int j, uint32_t any) {
-    while (any != 0u) {
-      const int e = __ffs(any) - 1;
-      any &= any - 1u;
-      float f = get_elem(v, e, static_cast<E*>(nullptr));
-      f = BWD ? apply_slope(q.rho, f, E::load_scalar_coherent(t.x + j + e)) : apply_rules(q, f, words[j - c0 + e]);
-      set_elem(v, e, f, static_cast<E*>(nullptr));
-    }
-  };
-
-  for (int rr = 0; rr < nrows; ++rr) {
-    const Part cur = part_of(rr);
-    uint4 v[kPer];
-    const uint32_t allowed = load(cur, v);
     if (used) {
       const int n = counted ? sh_len[rr] : 0;
       if (rr == 0 || n < held || n > win + kWindow) {
@@ -284,38 +236,62 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
       }
     }
 
-    auto scalar = [&](int j) {
-      const bool hit = used && (touched[(j - c0) >> 5] >> ((j - c0) & 31) & 1u);
-      float f = BWD ? 0.f : -INFINITY;
-      if (cur.m == nullptr || (bits_at(cur.m, j, mwords) & 1u) != 0) {
-        f = E::load_scalar_coherent(cur.src + j);
-        if (hit) f = BWD ? apply_slope(q.rho, f, E::load_scalar_coherent(cur.x + j)) : apply_rules(q, f, words[j - c0]);
-      }
-      E::store_scalar(cur.out + j, f);
+    // the touched column of this thread, loaded ahead of the copy
+    const int nt = used ? sh_touched : 0;
+    const S* x = BWD ? static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl : src;
+    struct Hit {
+      int j;  // the column, -1: none of this tile's, or forbidden
+      int col;
+      float f, x;
     };
-    // the scalar head and tail, at most one element per thread
-    int edge = tid < cur.sp.head ? tid : -1;
-    if (tid >= kRulesThreads - cur.sp.tail) edge = V - kRulesThreads + tid;
-    if (edge >= c0 && edge < c0 + W) scalar(edge);
+    auto look = [&](int t) {
+      Hit h{-1, t, 0.f, 0.f};
+      if (nt <= kListed) h.col = listed[t];
+      else if ((touched[t >> 5] >> (t & 31) & 1u) == 0) return h;
+      const int j = c0 + h.col;
+      if (j >= V) return h;
+      int first = j;  // the column that decides whose it is
+      if (j >= sp.head && j < sp.head + sp.nvec * VEC) first = j - (j - sp.head) % VEC;
+      if (first < c0 || first >= c0 + W) return h;
+      if (m != nullptr && (bits_at(m, j, mwords) & 1u) == 0) return h;
+      h.f = E::load_scalar_coherent(src + j);
+      if (BWD) h.x = E::load_scalar_coherent(x + j);
+      h.j = j;
+      return h;
+    };
+    const int todo = nt <= kListed ? nt : COLS;
+    Hit mine{-1, 0, 0.f, 0.f};
+    if (nt > 0 && tid < todo) mine = look(tid);
 
-    uint4* ob = reinterpret_cast<uint4*>(cur.out + cur.sp.head);
+    // the copy: the scalar head and tail (at most one element per thread), then the vectors
+    int edge = tid < sp.head ? tid : -1;
+    if (tid >= kRulesThreads - sp.tail) edge = V - kRulesThreads + tid;
+    if (edge >= c0 && edge < c0 + W) {
+      if (m != nullptr && (bits_at(m, edge, mwords) & 1u) == 0) E::store_bits(out + edge, kForbidden);
+      else if (!INPLACE) E::store_scalar(out + edge, E::load_scalar_coherent(src + edge));
+    }
+    uint4* ob = reinterpret_cast<uint4*>(out + sp.head);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int i = cur.i0 + tid + k * kRulesThreads;
-      if (i >= cur.i1) continue;
-      const int j = cur.sp.head + i * VEC;
-      const uint32_t ok = allowed >> (8 * k) & kAll;
-      const uint32_t any = used ? bits_at(touched, j - c0, MAPW) & ok : 0u;
-      if (INPLACE) {
-        if (any == 0u && ok == kAll) continue;  // the output is the input already
-        v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (ok != 0u) v[k] = load_any<E>(cur.src + cur.sp.head, i, same_phase);
+      const int i = i0 + tid + k * kRulesThreads;
+      if (i >= i1 || (INPLACE && full(k))) continue;
+      if (!full(k)) {
+        if (none(k)) v[k] = make_uint4(kForbidden, kForbidden, kForbidden, kForbidden);
+        else forbid(v[k], allowed >> (8 * k), kForbidden, static_cast<E*>(nullptr));
       }
-      if (any != 0u) touch(cur, v[k], j, any);
-      if (ok != kAll)
-        forbid(v[k], ok, BWD ? 0u : (sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u), static_cast<E*>(nullptr));
       st_v4_evict_first(ob + i, v[k]);
     }
+
+    // the touched columns over the copy
+    if (nt == 0) continue;
+    __syncthreads();
+    auto put = [&](const Hit& h) {
+      if (h.j < 0) return;
+      const float f = BWD ? (h.x > 0.f ? __fdiv_rn(h.f, q.rho) : h.f * q.rho) : apply_rules(q, h.f, words[h.col]);
+      E::store_scalar(out + h.j, f);
+    };
+    put(mine);
+    for (int t = tid + kRulesThreads; t < todo; t += kRulesThreads) put(look(t));
   }
 }
 

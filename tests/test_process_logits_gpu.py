@@ -153,9 +153,8 @@ def test_in_place_equals_out_of_place(dtype, layout):
         dx = dy.clone()
         rp.process_logits_bwd(x, dx, **d, dlogits=dx)
         same_bits(dx, want, "in place over dout")
-        y, _ = place(x.cpu(), layout)
-        rp.process_logits_bwd(y, dy, **d, dlogits=y)
-        same_bits(y, want, "in place over the logits")
+        with pytest.raises(rp.GrpoError):       # not over the logits
+            rp.process_logits_bwd(x, dy, **d, dlogits=x)
     untouched(buf, x)
 
 
@@ -205,6 +204,18 @@ def test_ids_and_lengths_out_of_range():
     k = make_rules(2, 3, V, 8, mask=False)
     k["prompt_len"][:] = [-5, 1 << 20]          # a prompt length is only compared
     assert check(x, k, what="prompt_len")[2] == 0
+
+
+def test_more_touched_columns_than_are_listed():
+    """Histories that touch most columns of a tile."""
+    V = 9000
+    x, _ = place((randn(2, 3, V, seed=1) * 2).to(torch.bfloat16), "odd")
+    k = make_rules(2, 3, V, 1, N=20000, growing=False)
+    k["hist_len"][:] = [20000, 19000, 2500, 0, 2000, 2300]
+    check(x, k, "phase", "many touched")
+    y = x.clone()
+    rp.process_logits_fwd(y, **on_gpu(k), out=y)
+    same_bits(y, rp.process_logits_fwd(x, **on_gpu(k)), "in place")
 
 
 def test_shared_histories_and_masks():
