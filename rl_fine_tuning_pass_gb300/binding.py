@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -95,13 +96,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "grpo_fused_linear_noalloc": [_P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
                                       _P, _P, _P, _P, _F, _F, _F, _F, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P,
                                       _P, _P],
-        "process_logits_fwd": [rows_p, ctypes.POINTER(GrpoLogitRules), rows_p, _P, _P],
-        "process_logits_bwd": [rows_p, rows_p, ctypes.POINTER(GrpoLogitRules), rows_p, _P, _P],
-        "topk_log_softmax": [rows_p, ctypes.c_int64, _F, _P, _P, _P, _P],
-        "distill_topk_fwd": [rows_p, _P, _P, ctypes.c_int64, _P, _F, _F, ctypes.c_int32, _P, _P, _P, _P, _P],
-        "distill_topk_bwd": [rows_p, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _F, _F, ctypes.c_int32, rows_p, _P],
-        "distill_topk_fused": [rows_p, _P, _P, ctypes.c_int64, _P, _P, _F, _F, ctypes.c_int32, _P, _P, _P, rows_p, _P,
-                               _P],
+        # descriptors as packed bytes (see _pack_rows), or byref of the structures
+        "process_logits_fwd": [_P, _P, _P, _P, _P],
+        "process_logits_bwd": [_P, _P, _P, _P, _P, _P],
+        "topk_log_softmax": [_P, ctypes.c_int64, _F, _P, _P, _P, _P],
+        "distill_topk_fwd": [_P, _P, _P, ctypes.c_int64, _P, _F, _F, ctypes.c_int32, _P, _P, _P, _P, _P],
+        "distill_topk_bwd": [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _F, _F, ctypes.c_int32, _P, _P],
+        "distill_topk_fused": [_P, _P, _P, ctypes.c_int64, _P, _P, _F, _F, ctypes.c_int32, _P, _P, _P, _P, _P, _P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -465,72 +466,112 @@ def grpo_fused_linear(hidden, weight, idx, adv, dloss, *, B, L, T, beta, eps_low
 # the sampler's rules on logits; a teacher's top log-probs; distillation from them
 # ---------------------------------------------------------------------------
 
+# A decode step calls these for microseconds of GPU work, so their marshalling is kept short:
+# descriptors are packed with ``struct`` (0.3 us; a ctypes structure takes 1.2 us), and the
+# stream and device are asked of torch's C layer (0.1 us each; torch.cuda's objects take 2 us).
+_ROWS = struct.Struct("=Qiiqqqqq")
+_RULES = struct.Struct("=QqqQQQQQQQqQqq")
+assert _ROWS.size == ctypes.sizeof(GrpoRows) and _RULES.size == ctypes.sizeof(GrpoLogitRules)
+_DTYPES = {torch.bfloat16: GRPO_BF16, torch.float32: GRPO_FP32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_device = torch._C._cuda_getDevice
+
+
+def _pack_rows(t: torch.Tensor):
+    """(packed grpo_rows, B, L, V) of a [B, L, V] (or [R, V], read as B=1, L=R) tensor."""
+    shape, stride, dt = t.shape, t.stride(), _DTYPES.get(t.dtype)
+    if dt is None or not t.is_cuda or not 2 <= len(shape) <= 3 or stride[-1] != 1:
+        if not t.is_cuda:
+            raise ValueError("logits must be a CUDA tensor")
+        rows_of(t)  # raises, but for a tensor whose vocabulary stride does not matter
+        stride = (*stride[:-1], 1)
+    if len(shape) == 3:
+        B, L, V = shape
+        sb, sl, _ = stride
+    else:
+        (L, V), B = shape, 1
+        sl = stride[0]
+        sb = L * sl
+    return _ROWS.pack(t.data_ptr(), dt, 0, B, L, V, sb, sl), B, L, V
+
+
 def _on(t: Optional[torch.Tensor], dtype, n: Optional[int], name: str, dev):
-    """``_ptr`` for a tensor that has to be on the logits' device."""
+    """``_ptr`` for a tensor that has to be on the logits' device (0 for None)."""
     if t is None:
-        return None
-    p = _ptr(t, dtype, n, name)
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    return p
+        return 0
+    if t.dtype is dtype and t.device == dev and t.is_contiguous() and (n is None or t.numel() == n):
+        return t.data_ptr()
+    _ptr(t, dtype, n, name)
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
-def _like(t: torch.Tensor, logits: torch.Tensor, name: str):
-    """A second [B, L, V] tensor of the call, described for C."""
-    if t.device != logits.device:
+def _like(t: Optional[torch.Tensor], logits: torch.Tensor, name: str):
+    """A second [B, L, V] tensor of the call (allocated like the logits if None) and its
+    descriptor."""
+    if t is None:
+        t = torch.empty_like(logits) if logits.is_contiguous() else \
+            torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    elif t.device != logits.device:
         raise ValueError(f"{name} must be on {logits.device}, got {t.device}")
-    return rows_of(t)
+    return t, _pack_rows(t)[0]
 
 
 def _call(fn: str, dev, *args):
     """Call the C entry point with the device's current stream, on that device."""
-    lib = load_library()
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(lib, fn)(*args, _stream(dev))
+    f = getattr(_lib or load_library(), fn)
+    index = dev.index
+    if _raw_device() == index:
+        st = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib, fn)(*args, _stream(dev))
-    _check(fn, st)
+            st = f(*args, _raw_stream(index))
+    if st != GRPO_OK:
+        raise GrpoError(fn, st)
 
 
 def _rules(B, L, V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed):
-    q = GrpoLogitRules()
+    tk = ts = N = ids = bs = M = al = sb = sl = 0
     if tokens is not None:
         if tokens.dim() != 2 or tokens.shape[0] != B or tokens.dtype != torch.int64 or tokens.device != dev:
             raise ValueError(f"tokens must be a [B, N] int64 tensor on {dev}")
-        if tokens.shape[1] > 1 and tokens.stride(1) != 1:
+        ts, one = tokens.stride()
+        N = tokens.shape[1]
+        if N > 1 and one != 1:
             raise ValueError("tokens must have stride 1 along a sequence")
-        q.tokens, q.tokens_stride, q.N = tokens.data_ptr(), tokens.stride(0), tokens.shape[1]
+        tk = tokens.data_ptr()
     elif hist_len is not None or prompt_len is not None or repetition is not None or frequency is not None \
             or presence is not None:
         raise ValueError("penalties and history lengths need tokens")
-    q.hist_len = _on(hist_len, torch.int32, B * L, "hist_len", dev)
-    q.prompt_len = _on(prompt_len, torch.int32, B, "prompt_len", dev)
-    q.repetition = _on(repetition, torch.float32, B, "repetition", dev)
-    q.frequency = _on(frequency, torch.float32, B, "frequency", dev)
-    q.presence = _on(presence, torch.float32, B, "presence", dev)
+    f32 = torch.float32
+    hist = _on(hist_len, torch.int32, B * L, "hist_len", dev)
+    prompt = _on(prompt_len, torch.int32, B, "prompt_len", dev)
+    rep = _on(repetition, f32, B, "repetition", dev)
+    freq = _on(frequency, f32, B, "frequency", dev)
+    pres = _on(presence, f32, B, "presence", dev)
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias_ids and bias go together")
     if bias_ids is not None:
-        if bias_ids.dim() != 2 or bias_ids.shape[0] != B or tuple(bias.shape) != tuple(bias_ids.shape):
+        shape = bias_ids.shape
+        if len(shape) != 2 or shape[0] != B or bias.shape != shape:
             raise ValueError("bias_ids and bias must be [B, M]")
-        q.bias_ids = _on(bias_ids, torch.int64, None, "bias_ids", dev)
-        q.bias = _on(bias, torch.float32, None, "bias", dev)
-        q.M = bias_ids.shape[1]
+        ids = _on(bias_ids, torch.int64, None, "bias_ids", dev)
+        bs = _on(bias, f32, None, "bias", dev)
+        M = shape[1]
     if allowed is not None:
         words = (V + 31) // 32
-        if allowed.dim() == 2 and allowed.shape[0] == B * L:
-            sb, sl = L * allowed.stride(0), allowed.stride(0)
-        elif allowed.dim() == 3 and tuple(allowed.shape[:2]) == (B, L):
-            sb, sl = allowed.stride(0), allowed.stride(1)
+        shape, stride = allowed.shape, allowed.stride()
+        if len(shape) == 2 and shape[0] == B * L:
+            sb, sl = L * stride[0], stride[0]
+        elif len(shape) == 3 and shape[0] == B and shape[1] == L:
+            sb, sl = stride[0], stride[1]
         else:
             raise ValueError("allowed must be [B*L, W] or [B, L, W]")
         if allowed.dtype != torch.int32 or allowed.device != dev:
             raise ValueError(f"allowed must be an int32 tensor on {dev}")
-        if allowed.shape[-1] < words or (words > 1 and allowed.stride(-1) != 1):
+        if shape[-1] < words or (words > 1 and stride[-1] != 1):
             raise ValueError(f"allowed needs {words} words a row, with stride 1")
-        q.allowed, q.allowed_stride_b, q.allowed_stride_l = allowed.data_ptr(), sb, sl
-    return q
+        al = allowed.data_ptr()
+    return _RULES.pack(tk, ts, N, hist, prompt, rep, freq, pres, ids, bs, M, al, sb, sl)
 
 
 def process_logits_fwd(logits, *, tokens=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
@@ -541,14 +582,11 @@ def process_logits_fwd(logits, *, tokens=None, hist_len=None, prompt_len=None, r
     the allowed columns, int32 [B*L, ceil(V / 32)] or [B, L, ceil(V / 32)] (expanded views
     too).  A decode batch is [B, 1, V].  Returns the processed logits, allocated like logits
     unless given; ``out=logits`` works in place and touches only what the rules change."""
-    B, L = _shape(logits)
-    if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    x, B, L, V = _pack_rows(logits)
     dev = logits.device
-    x, y = rows_of(logits), _like(out, logits, "out")
-    q = _rules(B, L, x.V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed)
-    _call("process_logits_fwd", dev, ctypes.byref(x), ctypes.byref(q), ctypes.byref(y),
-          _on(dev_err, torch.int32, 1, "dev_err", dev))
+    out, y = _like(out, logits, "out")
+    q = _rules(B, L, V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed)
+    _call("process_logits_fwd", dev, x, q, y, _on(dev_err, torch.int32, 1, "dev_err", dev))
     return out
 
 
@@ -556,38 +594,35 @@ def process_logits_bwd(logits, dout, *, tokens=None, hist_len=None, prompt_len=N
                        presence=None, bias_ids=None, bias=None, allowed=None, dlogits=None, dev_err=None):
     """Gradient of the logits of process_logits_fwd from that of its output (dlogits allocated
     like logits unless given; ``dlogits=dout`` works in place)."""
-    B, L = _shape(logits)
-    if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    x, B, L, V = _pack_rows(logits)
     dev = logits.device
-    x, dy, dx = rows_of(logits), _like(dout, logits, "dout"), _like(dlogits, logits, "dlogits")
-    q = _rules(B, L, x.V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed)
-    _call("process_logits_bwd", dev, ctypes.byref(x), ctypes.byref(dy), ctypes.byref(q), ctypes.byref(dx),
-          _on(dev_err, torch.int32, 1, "dev_err", dev))
+    _, dy = _like(dout, logits, "dout")
+    dlogits, dx = _like(dlogits, logits, "dlogits")
+    q = _rules(B, L, V, dev, tokens, hist_len, prompt_len, repetition, frequency, presence, bias_ids, bias, allowed)
+    _call("process_logits_bwd", dev, x, dy, q, dx, _on(dev_err, torch.int32, 1, "dev_err", dev))
     return dlogits
 
 
 def topk_log_softmax(logits, K, *, T=1.0):
     """The K largest log-probs of each row: (ids [B*L, K] int64, logp [B*L, K] fp32, lse [B*L]
     fp32), by falling logit, ties by rising column.  1 <= K <= min(V, 256)."""
-    B, L = _shape(logits)
+    x, B, L, _ = _pack_rows(logits)
     dev = logits.device
-    x = rows_of(logits)
-    K = int(K)
+    R, K = B * L, int(K)
     n = max(K, 0)
-    ids = torch.empty(B * L, n, dtype=torch.int64, device=dev)
-    logp = torch.empty(B * L, n, dtype=torch.float32, device=dev)
-    lse = torch.empty(B * L, dtype=torch.float32, device=dev)
-    _call("topk_log_softmax", dev, ctypes.byref(x), K, float(T), ids.data_ptr(), logp.data_ptr(), lse.data_ptr())
+    ids = torch.empty((R, n), dtype=torch.int64, device=dev)
+    logp = torch.empty((R, n), dtype=torch.float32, device=dev)
+    lse = torch.empty(R, dtype=torch.float32, device=dev)
+    _call("topk_log_softmax", dev, x, K, T, ids.data_ptr(), logp.data_ptr(), lse.data_ptr())
     return ids, logp, lse
 
 
-def _list_of(logits, ids, teacher_logp, R):
-    if ids.dim() != 2 or ids.shape[0] != R or tuple(teacher_logp.shape) != tuple(ids.shape):
+def _list_of(ids, teacher_logp, R, dev):
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != R or teacher_logp.shape != shape:
         raise ValueError("ids and teacher_logp must be [B*L, K]")
-    dev = logits.device
     return (_on(ids, torch.int64, None, "ids", dev), _on(teacher_logp, torch.float32, None, "teacher_logp", dev),
-            ids.shape[1])
+            shape[1])
 
 
 def distill_topk_fwd(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, mask=None, dev_err=None):
@@ -596,33 +631,27 @@ def distill_topk_fwd(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, 
     beta 0: KL(teacher | student), 1: KL(student | teacher), between: the mixture's.  tail:
     the teacher's mass outside its list is one more bucket (needed at beta 1); without it the
     teacher is renormalised over the list."""
-    B, L = _shape(logits)
-    R = B * L
-    dev = logits.device
-    x = rows_of(logits)
-    pi, pt, K = _list_of(logits, ids, teacher_logp, R)
-    out = {k: torch.empty(R, dtype=torch.float32, device=dev) for k in ("loss", "lse", "p_rest")}
-    _call("distill_topk_fwd", dev, ctypes.byref(x), pi, pt, K, _on(mask, torch.uint8, R, "mask", dev), float(T),
-          float(beta), int(bool(tail)), out["loss"].data_ptr(), out["lse"].data_ptr(), out["p_rest"].data_ptr(),
-          _on(dev_err, torch.int32, 1, "dev_err", dev))
-    return out
+    x, B, L, _ = _pack_rows(logits)
+    R, dev = B * L, logits.device
+    pi, pt, K = _list_of(ids, teacher_logp, R, dev)
+    loss, lse, p_rest = torch.empty((3, R), dtype=torch.float32, device=dev).unbind(0)
+    _call("distill_topk_fwd", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev), T, beta, bool(tail),
+          loss.data_ptr(), lse.data_ptr(), p_rest.data_ptr(), _on(dev_err, torch.int32, 1, "dev_err", dev))
+    return {"loss": loss, "lse": lse, "p_rest": p_rest}
 
 
 def distill_topk_bwd(logits, ids, teacher_logp, dloss, lse, p_rest, *, T=1.0, beta=0.0, tail=False, mask=None,
                      dlogits=None):
     """dlogits of sum_r dloss_r * loss_r, with lse and p_rest of distill_topk_fwd (allocated
     like logits unless given; ``dlogits=logits`` works in place)."""
-    B, L = _shape(logits)
-    R = B * L
-    if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    dev = logits.device
-    x, dx = rows_of(logits), _like(dlogits, logits, "dlogits")
-    pi, pt, K = _list_of(logits, ids, teacher_logp, R)
-    f = lambda t, name: _on(t, torch.float32, R, name, dev)  # noqa: E731
-    _call("distill_topk_bwd", dev, ctypes.byref(x), pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
-          f(dloss, "dloss"), f(lse, "lse"), f(p_rest, "p_rest"), float(T), float(beta), int(bool(tail)),
-          ctypes.byref(dx))
+    x, B, L, _ = _pack_rows(logits)
+    R, dev = B * L, logits.device
+    dlogits, dx = _like(dlogits, logits, "dlogits")
+    pi, pt, K = _list_of(ids, teacher_logp, R, dev)
+    f32 = torch.float32
+    _call("distill_topk_bwd", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
+          _on(dloss, f32, R, "dloss", dev), _on(lse, f32, R, "lse", dev), _on(p_rest, f32, R, "p_rest", dev), T, beta,
+          bool(tail), dx)
     return dlogits
 
 
@@ -630,17 +659,12 @@ def distill_topk_fused(logits, ids, teacher_logp, dloss, *, T=1.0, beta=0.0, tai
                        dev_err=None):
     """distill_topk_fwd and distill_topk_bwd in one call, for loss weights dloss known in
     advance; returns the forward's dict plus "dlogits"."""
-    B, L = _shape(logits)
-    R = B * L
-    if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    dev = logits.device
-    x, dx = rows_of(logits), _like(dlogits, logits, "dlogits")
-    pi, pt, K = _list_of(logits, ids, teacher_logp, R)
-    out = {k: torch.empty(R, dtype=torch.float32, device=dev) for k in ("loss", "lse", "p_rest")}
-    _call("distill_topk_fused", dev, ctypes.byref(x), pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
-          _on(dloss, torch.float32, R, "dloss", dev), float(T), float(beta), int(bool(tail)), out["loss"].data_ptr(),
-          out["lse"].data_ptr(), out["p_rest"].data_ptr(), ctypes.byref(dx),
-          _on(dev_err, torch.int32, 1, "dev_err", dev))
-    out["dlogits"] = dlogits
-    return out
+    x, B, L, _ = _pack_rows(logits)
+    R, dev = B * L, logits.device
+    dlogits, dx = _like(dlogits, logits, "dlogits")
+    pi, pt, K = _list_of(ids, teacher_logp, R, dev)
+    loss, lse, p_rest = torch.empty((3, R), dtype=torch.float32, device=dev).unbind(0)
+    _call("distill_topk_fused", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
+          _on(dloss, torch.float32, R, "dloss", dev), T, beta, bool(tail), loss.data_ptr(), lse.data_ptr(),
+          p_rest.data_ptr(), dx, _on(dev_err, torch.int32, 1, "dev_err", dev))
+    return {"loss": loss, "lse": lse, "p_rest": p_rest, "dlogits": dlogits}

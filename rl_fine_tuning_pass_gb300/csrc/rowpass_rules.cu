@@ -306,10 +306,8 @@ cudaError_t launch_e(bool same_phase, const RulesParams& p, int64_t rows, int sm
   if (run > p.x.L) run = p.x.L;
   const int64_t runs = (p.x.L + run - 1) / run;
   const bool used = !BWD && (p.tokens != nullptr || p.M > 0);
-  const int most = (COLS + 3) / 4 * 16;
-  const cudaError_t e = cudaFuncSetAttribute(rules_kernel<E, BWD, INPLACE>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e != cudaSuccess) return e;
+  constexpr int most = (COLS + 3) / 4 * 16;
+  static_assert(most < 40 * 1024, "with the static part within the 48 KB that need no leave");
   const int64_t grid = rows / p.x.L * runs * tiles;
   return launch_after_previous_smem(rules_kernel<E, BWD, INPLACE>, dim3(static_cast<unsigned>(grid)),
                                     dim3(kRulesThreads), used ? most : 0, s, p, tiles, static_cast<int>(run),

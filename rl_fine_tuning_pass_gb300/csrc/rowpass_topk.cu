@@ -395,9 +395,11 @@ template <class E, int CS>
 cudaError_t launch_topk_cs(const TopkParams& p, int64_t rows, cudaStream_t s) {
   const int cap = p.K > 128 ? 4096 : 2048;
   const size_t smem = 8 * (static_cast<size_t>(cap) + kSurvivors + (CS > 1 ? CS * p.K : 0));
-  const cudaError_t e = cudaFuncSetAttribute(topk_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             8 * (4096 + kSurvivors + (CS > 1 ? CS * kTopkMax : 0)));
-  if (e != cudaSuccess) return e;
+  if (smem > 40 * 1024) {  // with the static part past the 48 KB that need no leave
+    const cudaError_t e = cudaFuncSetAttribute(topk_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               8 * (4096 + kSurvivors + (CS > 1 ? CS * kTopkMax : 0)));
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * CS));
   cfg.blockDim = dim3(kTopkThreads);

@@ -136,11 +136,26 @@ def test_python_rules_refused(kw, match):
         binding._rules(2, 3, 64, torch.device("cpu"), **{**full, **kw})
 
 
+def described(*args, **kw):
+    return binding.GrpoLogitRules.from_buffer_copy(binding._rules(*args, **kw))
+
+
+def test_rules_are_packed_as_the_c_structure():
+    t = lambda *n, dt=torch.float32: torch.zeros(*n, dtype=dt)  # noqa: E731
+    kw = dict(tokens=t(2, 9, dt=torch.int64)[:, :7], hist_len=t(6, dt=torch.int32), prompt_len=t(2, dt=torch.int32),
+              repetition=t(2), frequency=t(2), presence=t(2), bias_ids=t(2, 5, dt=torch.int64), bias=t(2, 5),
+              allowed=t(2, 3, 4, dt=torch.int32))
+    q = described(2, 3, 64, torch.device("cpu"), **kw)
+    for name, v in kw.items():
+        assert getattr(q, name) == v.data_ptr(), name
+    assert (q.tokens_stride, q.N, q.M, q.allowed_stride_b, q.allowed_stride_l) == (9, 7, 5, 12, 4)
+
+
 def test_expanded_masks_are_described_by_their_strides():
     full = dict.fromkeys(("tokens", "hist_len", "prompt_len", "repetition", "frequency", "presence", "bias_ids",
                           "bias"))
     one = torch.zeros(1, 1, 2, dtype=torch.int32)
-    q = binding._rules(2, 3, 64, torch.device("cpu"), allowed=one.expand(2, 3, 2), **full)
+    q = described(2, 3, 64, torch.device("cpu"), allowed=one.expand(2, 3, 2), **full)
     assert (q.allowed_stride_b, q.allowed_stride_l) == (0, 0)
-    q = binding._rules(2, 3, 64, torch.device("cpu"), allowed=torch.zeros(6, 5, dtype=torch.int32), **full)
+    q = described(2, 3, 64, torch.device("cpu"), allowed=torch.zeros(6, 5, dtype=torch.int32), **full)
     assert (q.allowed_stride_b, q.allowed_stride_l) == (15, 5)
