@@ -698,7 +698,8 @@ grpo::DistillParams distill_params(const grpo_rows* logits, const int64_t* ids, 
   p.K = static_cast<int>(K);
   p.mask = mask;
   p.c = static_cast<float>(kLog2eD / static_cast<double>(T));
-  p.invT = 1.0 / static_cast<double>(T);
+  p.invT = static_cast<float>(1.0 / static_cast<double>(T));
+  p.invT_lo = static_cast<float>(1.0 / static_cast<double>(T) - static_cast<double>(p.invT));
   p.T = T;
   p.beta = beta;
   p.tail = tail != 0;

@@ -67,7 +67,7 @@ struct DistillParams {
   const uint8_t* mask;   // nullable
   const float* dloss;    // backward, fused
   float c;               // log2(e) / T
-  double invT;
+  float invT, invT_lo;   // 1 / T, and what its rounding left
   float T;
   float beta;
   int tail;

@@ -12,11 +12,17 @@
 // elements written after it.  p_rest is summed from the columns outside the list (a bitmap in
 // shared memory leaves the listed ones out of the stream), not taken from 1 - sum p_k: it keeps
 // its relative accuracy when the list holds nearly all of the mass.
+//
+// A CTA takes a row.  Its last warp, the list warp, does not stream: it reads the list, marks the
+// bitmap, and works out what the teacher says (with 64-bit exponentials, the rest's mass being
+// 1 - sum q_k) while the others stream the row; then it finishes the row from their statistic.
+// log-probs of the buckets are formed from differences x_k - max in fp32 with a correction term:
+// an error that all buckets share cancels in the loss (below) and in the gradient.
 #pragma once
 
 #include "logits_ops.h"
 #include "logits_stat.cuh"
-#include "rowpass_bwd.cuh"
+#include "rowpass_fused.cuh"
 
 namespace grpo {
 namespace {
@@ -27,22 +33,35 @@ constexpr double kRestMin = 0x1p-20;     // least teacher mass outside the list
 // The list of one row in shared memory.  id -1: an unused slot.
 struct Slots {
   int* id;
-  float* lq;  // teacher log-prob as given; later G_k - p_k S, scaled
-  float* x;   // the student's logit
+  float* lq;  // teacher log-prob as given; later G_k
+  float* x;   // the student's logit; later p_k
 };
+__device__ __forceinline__ Slots slots_at(void* at, int K) {
+  Slots sl;
+  sl.id = static_cast<int*>(at);
+  sl.lq = reinterpret_cast<float*>(sl.id + K);
+  sl.x = sl.lq + K;
+  return sl;
+}
 
 // Terms of one bucket: its part of the loss and G.  r = log q - log p, which carries the
-// precision where p and q are near each other.
+// precision where p and q are near each other.  The parts of the loss carry (p - q) or (q - p)
+// besides (they sum to nothing over the buckets, `row_loss` takes out what is left): an error of
+// r then enters times p - q, so one that all buckets share, such as that of log s, does not count.
 struct Term {
   float loss, G;
 };
 __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
   Term t;
   if (beta == 0.f) {
-    t.loss = q == 0.f ? 0.f : q * r;
-    t.G = fabsf(r) < 0.5f ? -p * expm1f(r) : p - q;  // p (1 - q / p)
+    const bool near = fabsf(r) < 0.5f;
+    const float e = expm1f(near ? r : 0.f);
+    t.G = near ? -p * e : p - q;  // p (1 - q / p)
+    t.loss = q == 0.f ? p : (near ? q * (expm1f(-r) + r) : q * r - q + p);
   } else if (beta == 1.f) {
-    t.loss = t.G = p == 0.f ? 0.f : -p * r;
+    const bool near = fabsf(r) < 0.5f;
+    t.G = p == 0.f ? 0.f : -p * r;
+    t.loss = p == 0.f ? q : (near ? p * (expm1f(r) - r) : t.G - p + q);
   } else {
     // log(p/m) and log(q/m) from r alone: m/p = 1 + beta (e^r - 1), m/q = 1 + (1 - beta)(e^-r - 1)
     float lpm, lqm;
@@ -58,11 +77,9 @@ __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
   }
   return t;
 }
-
-// log(q / p) of the rest, from masses held in 64 bits.
-__device__ __forceinline__ float rest_ratio(double q, double p) {
-  const float d = static_cast<float>((q - p) / p);
-  return fabsf(d) < 0.5f ? log1pf(d) : logf(static_cast<float>(q / p));
+// The loss from the sum of its parts; over = sum q - 1.
+__device__ __forceinline__ float row_loss(float parts, float over, float beta) {
+  return beta == 0.f ? parts + over : (beta == 1.f ? parts - over : parts);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -77,91 +94,124 @@ __device__ __forceinline__ T warp_sum(T v) {
   return v;
 }
 
-// What the teacher's list says: log q_k = lq_k - shift, and the mass outside the list.  One
-// warp; the sums over the list in 64 bits, since q_rest = 1 - sum q_k cancels.
+// d / T as a value and what its rounding left.
+struct Scaled {
+  float hi, lo;
+};
+__device__ __forceinline__ Scaled over_T(float d, const DistillParams& p) {
+  Scaled z;
+  z.hi = d * p.invT;
+  z.lo = fmaf(d, p.invT, -z.hi) + d * p.invT_lo;
+  return z;
+}
+// e^(d / T), d <= 0 or small
+__device__ __forceinline__ float exp_over_T(float d, const DistillParams& p) {
+  const Scaled z = over_T(d, p);
+  const float e = expf(z.hi);
+  return fabsf(z.hi) < 1e30f ? fmaf(e, z.lo, e) : e;
+}
+
+// What the teacher's list says (one warp): log q_k = lq_k - shift, the mass of the list and
+// outside it, and sum q - 1.
 struct Teacher {
-  double shift, q_rest;
+  float shift, list, rest, over;
 };
 __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) {
   const int lane = threadIdx.x & 31;
-  Teacher t{0.0, 0.0};
+  Teacher t{0.f, 1.f, 0.f, 0.f};
   if (tail) {
     double sum = 0.0;
     for (int k = lane; k < K; k += 32)
       if (sl.id[k] >= 0) sum += exp(static_cast<double>(sl.lq[k]));
-    sum = 1.0 - warp_sum(sum);
-    t.q_rest = sum < kRestMin ? kRestMin : sum;  // a NaN stays one
+    sum = warp_sum(sum);
+    const double left = 1.0 - sum, rest = left < kRestMin ? kRestMin : left;  // a NaN stays one
+    t.list = static_cast<float>(sum);
+    t.rest = static_cast<float>(rest);
+    t.over = static_cast<float>(rest - left);
   } else {
     float m = -INFINITY;
     for (int k = lane; k < K; k += 32)
       if (sl.id[k] >= 0) m = fmaxf(m, sl.lq[k]);
     m = warp_max(m);
     float sum = 0.f;
+    int used = 0;
     for (int k = lane; k < K; k += 32)
-      if (sl.id[k] >= 0) sum += expf(sl.lq[k] - m);
-    t.shift = static_cast<double>(m) + log(static_cast<double>(warp_sum(sum)));
+      if (sl.id[k] >= 0) {
+        sum += expf(sl.lq[k] - m);
+        used = 1;
+      }
+    t.shift = m + logf(warp_sum(sum));
+    if (!__any_sync(0xFFFFFFFFu, used)) {  // nothing listed
+      t.list = 0.f;
+      t.over = -1.f;
+    }
   }
   return t;
 }
 
-// One row's results (every lane of the calling warp).
+// log(q / p) of the rest, d = q - p
+__device__ __forceinline__ float rest_ratio(float q, float p, float d) {
+  const float e = d / p;
+  return fabsf(e) < 0.5f ? log1pf(e) : logf(q / p);
+}
+
+// One row's results (every lane of the list warp); the slots then hold G_k and p_k.
 struct RowResult {
   float loss, lse, p_rest;
+  float m, inv_s;   // p_j = 2^((x_j - m) c) inv_s
   float S, F_rest;  // sum of G, G_rest / p_rest
 };
 
-// The slots and the rest of a row, from the statistic `st` of the columns outside the list
-// (every lane of one warp).  Log-probs of the buckets are formed in 64 bits: a divergence is
-// a small difference of numbers around 10.
-__device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const MaxStat& st, const DistillParams& p) {
+// The slots and the rest of a row, from the statistic `st` of the columns outside the list.
+__device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const Teacher& te, const MaxStat& st,
+                                                const DistillParams& p) {
   const int lane = threadIdx.x & 31;
-  const Teacher te = teacher_of(sl, K, p.tail);
-  float xm = -INFINITY;
+  float m = st.s != 0.f ? st.m : -FLT_MAX;
   for (int k = lane; k < K; k += 32)
-    if (sl.id[k] >= 0) xm = fmaxf(xm, sl.x[k]);
-  xm = warp_max(xm);
-  const bool any_rest = st.s != 0.f;
-  const double a = static_cast<double>(st.m) * p.invT;
-  double M = static_cast<double>(xm) * p.invT;
-  if (any_rest && !(a < M)) M = a;
-  const double s_rest = any_rest ? static_cast<double>(st.s) * exp(a - M) : 0.0;
-  double s = 0.0;
+    if (sl.id[k] >= 0) m = fmaxf(m, sl.x[k]);
+  m = warp_max(m);
+  const float s_rest = st.s == 0.f ? 0.f : st.s * exp_over_T(st.m - m, p);
+  float s_list = 0.f;
   for (int k = lane; k < K; k += 32)
-    if (sl.id[k] >= 0) s += static_cast<double>(expf(static_cast<float>(static_cast<double>(sl.x[k]) * p.invT - M)));
-  s = s_rest + warp_sum(s);
-  const double lse = M + log(s), inv_s = 1.0 / s;
+    if (sl.id[k] >= 0) s_list += exp_over_T(sl.x[k] - m, p);
+  s_list = warp_sum(s_list);
+  const float s = s_rest + s_list, inv_s = 1.f / s, ln_s = logf(s);
   float loss = 0.f, S = 0.f;
   for (int k = lane; k < K; k += 32) {
     if (sl.id[k] < 0) continue;
-    const double z = static_cast<double>(sl.x[k]) * p.invT;
-    const float pk = static_cast<float>(static_cast<double>(expf(static_cast<float>(z - M))) * inv_s);
-    const double lq = static_cast<double>(sl.lq[k]) - te.shift;
-    const Term t = bucket(expf(static_cast<float>(lq)), pk, static_cast<float>(lq - (z - lse)), p.beta);
+    const float d = sl.x[k] - m;
+    const Scaled z = over_T(d, p);
+    const float pk = exp_over_T(d, p) * inv_s, lq = sl.lq[k] - te.shift;
+    const Term t = bucket(expf(lq), pk, pk == 0.f ? INFINITY : ((lq - z.hi) + ln_s) - z.lo, p.beta);
     loss += t.loss;
     S += t.G;
+    sl.lq[k] = t.G;
+    sl.x[k] = pk;
   }
-  const double p_rest = s_rest * inv_s;
-  const Term t = bucket(static_cast<float>(te.q_rest), static_cast<float>(p_rest), rest_ratio(te.q_rest, p_rest),
-                        p.beta);
+  const float pr = s_rest * inv_s, pl = s_list * inv_s;
+  const float dr = pr > 0.5f && te.over == 0.f ? pl - te.list : te.rest - pr;  // q_rest - p_rest
+  const Term t = bucket(te.rest, pr, rest_ratio(te.rest, pr, dr), p.beta);
   RowResult o;
-  o.lse = static_cast<float>(lse);
-  // relative to the lse as it is stored: the backward's other p_j are too, and a common factor
+  const Scaled zm = over_T(m, p);
+  o.lse = zm.hi + ln_s;
+  // relative to the lse as it is stored: the backward's other p_j are too, and the common factor
   // cancels in its differences
-  const float d_lse = static_cast<float>(lse - static_cast<double>(o.lse));
-  o.p_rest = static_cast<float>(p_rest + p_rest * static_cast<double>(d_lse));
-  o.loss = warp_sum(loss) + t.loss;
+  o.p_rest = s_rest * expf((zm.hi - o.lse) + zm.lo);
+  o.loss = row_loss(warp_sum(loss) + t.loss, te.over, p.beta);
+  o.m = m;
+  o.inv_s = inv_s;
   o.S = warp_sum(S) + t.G;
-  o.F_rest = p_rest == 0.0 ? 0.f : t.G / static_cast<float>(p_rest);
+  o.F_rest = pr == 0.f ? 0.f : t.G / pr;
   return o;
 }
 
-// Load the row's list: ids (checked), teacher log-probs and the student's logits.  Returns
-// whether this thread met an id >= V.
-template <class E, int THREADS>
+// The row's list (one warp): ids, teacher log-probs and the student's logits.  Returns whether
+// this thread met an id >= V.
+template <class E>
 __device__ __forceinline__ bool load_slots(const Slots& sl, const DistillParams& p, int64_t r,
                                            const typename E::storage* row) {
   bool bad = false;
-  for (int k = threadIdx.x; k < p.K; k += THREADS) {
+  for (int k = threadIdx.x & 31; k < p.K; k += 32) {
     const int64_t id = p.ids[r * p.K + k];
     const bool in = id >= 0 && id < p.x.V;
     bad |= id >= p.x.V;
@@ -230,95 +280,12 @@ __host__ __device__ inline int bitmap_bytes(int V) {
   return need < kBitmapBytes ? static_cast<int>(need) : kBitmapBytes;
 }
 
-template <class E, int THREADS, int UNROLL>
-__global__ void __launch_bounds__(THREADS) distill_fwd_kernel(const DistillParams p, int bm_bytes) {
-  using S = typename E::storage;
-  extern __shared__ uint4 distill_smem[];
-  __shared__ int sh_bad;
-  wait_for_previous_grids();
-  const int64_t r = blockIdx.x;
-  const int64_t b = r / p.x.L, l = r - b * p.x.L;
-  const int tid = threadIdx.x, V = p.x.V, K = p.K;
-  if (p.mask != nullptr && p.mask[r] == 0) {
-    if (tid == 0) {
-      p.loss[r] = 0.f;
-      p.lse[r] = 0.f;
-      p.p_rest[r] = 0.f;
-    }
-    return;
-  }
-  const S* row = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
-  const RowSplit sp = split_row<E>(row, V);
-  Slots sl;
-  sl.id = reinterpret_cast<int*>(reinterpret_cast<char*>(distill_smem) + bm_bytes);
-  sl.lq = reinterpret_cast<float*>(sl.id + K);
-  sl.x = sl.lq + K;
-  Bitmap<E> bm;
-  bm.w = reinterpret_cast<uint32_t*>(distill_smem);
-  bm.mask = V + 2 * E::kVec > bm_bytes * 8 ? static_cast<uint32_t>(bm_bytes) * 8u - 1u : 0xFFFFFFFFu;
-  bm.head = sp.head;
-
-  for (int i = tid; i < bm_bytes / 16; i += THREADS) distill_smem[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (tid == 0) sh_bad = 0;
-  bool bad = load_slots<E, THREADS>(sl, p, r, row);
-  if (bad && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
-  __syncthreads();
-  for (int k = tid; k < K; k += THREADS) {
-    const int id = sl.id[k];
-    if (id < 0 || !bm.set(id)) continue;
-    bool twice = !bm.wraps();
-    for (int q = 0; !twice && q < K; ++q) twice = q != k && sl.id[q] == id;
-    if (twice && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_DUPLICATE_ID_BIT);
-    bad |= twice;
-  }
-  if (bad) sh_bad = 1;
-  __syncthreads();
-
-  const float c = p.c;
-  MaxRun rs;
-  auto scalar = [&](int j) {
-    if (bm.get(j) && (!bm.wraps() || listed_bits(sl, K, j, 1))) return;
-    maxrun_scalar(rs, E::load_scalar(row + j), c);
-  };
-  if (tid < sp.head) scalar(tid);
-  if (tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
-  auto leave_out = [&](uint4& v, int i) {
-    uint32_t bits = bm.vec(i);
-    if (bits != 0u) {
-      if (bm.wraps()) bits = listed_bits(sl, K, sp.head + i * E::kVec, E::kVec);
-      drop(v, bits, static_cast<E*>(nullptr));
-    }
-  };
-  const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
-  int i = tid;
-  for (; i + (UNROLL - 1) * THREADS < sp.nvec; i += UNROLL * THREADS) {
-    uint4 v[UNROLL];
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k) v[k] = ld_nc_v4(vb + i + k * THREADS);
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k) leave_out(v[k], i + k * THREADS);
-    maxrun_vectors<E>(rs, v, c);
-  }
-  for (; i < sp.nvec; i += THREADS) {
-    uint4 v[1] = {ld_nc_v4(vb + i)};
-    leave_out(v[0], i);
-    maxrun_vectors<E>(rs, v, c);
-  }
-  const MaxStat st = maxstat_block<THREADS>(rs.stat(), c);
-  if (tid >= 32) return;
-  const RowResult o = finish_row(sl, K, st, p);
-  if (tid == 0) {
-    const float nan = __int_as_float(0x7FC00000);
-    p.loss[r] = sh_bad ? nan : o.loss;
-    p.lse[r] = sh_bad ? nan : o.lse;
-    p.p_rest[r] = sh_bad ? nan : o.p_rest;
-  }
-}
-
-// out_j = f 2^((x_j - x0) c) over the row.
+// out_j = f 2^((x_j - x0) c) over the row (the streaming threads).  With kept_vecs > 0, body
+// vectors [0, kept_vecs) come from `kept` in shared memory, after the others.
 template <class E, int THREADS, int UNROLL, bool SAME_PHASE>
 __device__ __forceinline__ void grad_stream(const typename E::storage* in, typename E::storage* out,
-                                            const RowSplit& sp, float x0, float c, float f) {
+                                            const RowSplit& sp, float x0, float c, float f,
+                                            const uint4* kept = nullptr, int kept_vecs = 0) {
   const int tid = threadIdx.x;
   auto scalar = [&](int j) { E::store_scalar(out + j, f * ex2((E::load_scalar_coherent(in + j) - x0) * c)); };
   if (tid < sp.head) scalar(tid);
@@ -335,21 +302,170 @@ __device__ __forceinline__ void grad_stream(const typename E::storage* in, typen
     }
     st_v4_evict_first(ob + i, E::template pack_pairs<false>(d));
   };
-  int i = tid;
-  for (; i + (UNROLL - 1) * THREADS < sp.nvec; i += UNROLL * THREADS) {
-    uint4 v[UNROLL];
+  auto sweep = [&](auto load, int i, int n) {
+    for (; i + (UNROLL - 1) * THREADS < n; i += UNROLL * THREADS) {
+      uint4 v[UNROLL];
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) v[k] = load_vec<E, SAME_PHASE, true>(ib, i + k * THREADS);
+      for (int k = 0; k < UNROLL; ++k) v[k] = load(i + k * THREADS);
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) process(v[k], i + k * THREADS);
-  }
-  for (; i < sp.nvec; i += THREADS) process(load_vec<E, SAME_PHASE, true>(ib, i), i);
+      for (int k = 0; k < UNROLL; ++k) process(v[k], i + k * THREADS);
+    }
+    for (; i < n; i += THREADS) process(load(i), i);
+  };
+  sweep([&](int j) { return load_vec<E, SAME_PHASE, true>(ib, j); }, kept_vecs + tid, sp.nvec);
+  if (kept_vecs > 0) sweep([&](int j) { return kept[j]; }, tid, kept_vecs);
 }
 
-// The backward: one warp works out the row's factor and the listed columns' gradients while
-// they are few, then the row is streamed as in rowgrad_kernel.
+// Forward, or (FUSED) forward and backward in one kernel: the row is swept again for the gradient
+// once its factor is known, from L2 or (long rows, 512 threads) from the part kept in shared
+// memory, as in fused_kernel.
+template <class E, int THREADS, int UNROLL, bool FUSED, bool SAME_PHASE>
+__global__ void __launch_bounds__(THREADS + 32) distill_kernel(const DistillParams p, int bm_bytes, int keep_vecs) {
+  using S = typename E::storage;
+  constexpr int kWarps = THREADS / 32;
+  extern __shared__ uint4 distill_smem[];
+  __shared__ MaxStat sh_stat[kWarps];
+  __shared__ float sh_factor, sh_m;
+  __shared__ __align__(8) uint64_t kept_bar;
+  wait_for_previous_grids();
+  const int64_t r = blockIdx.x;
+  const int64_t b = r / p.x.L, l = r - b * p.x.L;
+  const int tid = threadIdx.x, V = p.x.V, K = p.K;
+  const bool list_warp = tid >= THREADS;
+  S* out = FUSED ? static_cast<S*>(p.dx.ptr) + b * p.dx.sb + l * p.dx.sl : nullptr;
+  if (p.mask != nullptr && p.mask[r] == 0) {
+    if (tid == 0) {
+      p.loss[r] = 0.f;
+      p.lse[r] = 0.f;
+      p.p_rest[r] = 0.f;
+    }
+    if (FUSED && !list_warp) {
+      const RowSplit osp = split_row<E>(out, V);
+      fill_span<E, THREADS>(out, osp, whole_row(osp), 0u);
+    }
+    return;
+  }
+  const S* row = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
+  const RowSplit sp = split_row<E>(row, V);
+  uint4* kept = distill_smem;
+  uint4* bits = kept + (FUSED ? keep_vecs : 0);
+  const Slots sl = slots_at(reinterpret_cast<char*>(bits) + bm_bytes, K);
+  Bitmap<E> bm;
+  bm.w = reinterpret_cast<uint32_t*>(bits);
+  bm.mask = V + 2 * E::kVec > bm_bytes * 8 ? static_cast<uint32_t>(bm_bytes) * 8u - 1u : 0xFFFFFFFFu;
+  bm.head = sp.head;
+  const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
+  const int kv = FUSED && SAME_PHASE ? min(keep_vecs, sp.nvec) : 0;
+  const uint32_t bar = smem_addr(&kept_bar);
+  if (FUSED && kv > 0 && tid == 0) kept_copy_issue(bar, smem_addr(kept), vb, static_cast<uint32_t>(kv) * 16u);
+
+  bool bad = false;
+  if (list_warp) {
+    bad = load_slots<E>(sl, p, r, row);
+    if (bad && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
+  } else {
+    for (int i = tid; i < bm_bytes / 16; i += THREADS) bits[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  if (list_warp) {
+    for (int k = tid - THREADS; k < K; k += 32) {
+      const int id = sl.id[k];
+      if (id < 0 || !bm.set(id)) continue;
+      bool twice = !bm.wraps();
+      for (int q = 0; !twice && q < K; ++q) twice = q != k && sl.id[q] == id;
+      if (twice && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_DUPLICATE_ID_BIT);
+      bad |= twice;
+    }
+  }
+  __syncthreads();
+
+  Teacher te{};
+  const float c = p.c;
+  if (list_warp) {
+    te = teacher_of(sl, K, p.tail);
+  } else {
+    MaxRun rs;
+    auto scalar = [&](int j) {
+      if (bm.get(j) && (!bm.wraps() || listed_bits(sl, K, j, 1))) return;
+      maxrun_scalar(rs, FUSED ? E::load_scalar_coherent(row + j) : E::load_scalar(row + j), c);
+    };
+    if (tid < sp.head) scalar(tid);
+    if (tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
+    auto leave_out = [&](uint4& v, int i) {
+      uint32_t w = bm.vec(i);
+      if (w != 0u) {
+        if (bm.wraps()) w = listed_bits(sl, K, sp.head + i * E::kVec, E::kVec);
+        drop(v, w, static_cast<E*>(nullptr));
+      }
+    };
+    auto sweep = [&](auto load, int i, int n) {
+      for (; i + (UNROLL - 1) * THREADS < n; i += UNROLL * THREADS) {
+        uint4 v[UNROLL];
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) v[k] = load(i + k * THREADS);
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) leave_out(v[k], i + k * THREADS);
+        maxrun_vectors<E>(rs, v, c);
+      }
+      for (; i < n; i += THREADS) {
+        uint4 v[1] = {load(i)};
+        leave_out(v[0], i);
+        maxrun_vectors<E>(rs, v, c);
+      }
+    };
+    // FUSED: coherent loads (dlogits may alias the logits), kept in L2 for the second sweep
+    sweep([&](int i) { return FUSED ? ld_v4_evict_last(vb + i) : ld_nc_v4(vb + i); }, kv + tid, sp.nvec);
+    if (FUSED && kv > 0) {
+      if (!kept_copy_wait(bar)) {  // the row's outputs are not valid; wait once more for the copies in flight
+        if (tid == 0 && p.dev_err != nullptr) atomicOr(p.dev_err, GRPO_DEVERR_TIMEOUT_BIT);
+        kept_copy_wait(bar);
+      }
+      sweep([&](int i) { return kept[i]; }, tid, kv);
+    }
+    const MaxStat st = maxstat_warp(rs.stat(), c);
+    if ((tid & 31) == 0) sh_stat[tid >> 5] = st;
+  }
+  __syncthreads();
+  if (list_warp) {
+    const int lane = tid - THREADS;
+    const MaxStat st = maxstat_warp(lane < kWarps ? sh_stat[lane] : MaxStat{-FLT_MAX, 0.f}, c);
+    const float g = FUSED ? p.dloss[r] / p.T : 0.f;
+    const RowResult o = finish_row(sl, K, te, st, p);
+    const float nan = __int_as_float(0x7FC00000);
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (lane == 0) {
+      p.loss[r] = bad ? nan : o.loss;
+      p.lse[r] = bad ? nan : o.lse;
+      p.p_rest[r] = bad ? nan : o.p_rest;
+    }
+    if (FUSED) {
+      for (int k = lane; k < K; k += 32) sl.lq[k] = bad ? nan : g * (sl.lq[k] - sl.x[k] * o.S);
+      if (lane == 0) {
+        sh_factor = g == 0.f ? 0.f : (bad ? nan : g * (o.F_rest - o.S) * o.inv_s);
+        sh_m = o.m;
+        sh_stat[0].s = g;
+      }
+    }
+  }
+  if (!FUSED) return;
+  __syncthreads();
+  const RowSplit osp = split_row<E>(out, V);
+  const float f = sh_factor, g = sh_stat[0].s;
+  if (!list_warp) {
+    if (f == 0.f) fill_span<E, THREADS>(out, osp, whole_row(osp), 0u);
+    else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, osp, sh_m, c, f, kept, kv);
+  }
+  if (g == 0.f) return;  // +0.0 everywhere
+  __syncthreads();       // the listed columns' values go over the stream's
+  if (list_warp)
+    for (int k = tid - THREADS; k < K; k += 32)
+      if (sl.id[k] >= 0) E::store_scalar(out + sl.id[k], sl.lq[k]);
+}
+
+// The backward: the list warp works out the row's factor and the listed columns' gradients, then
+// the others stream the row as rowgrad_kernel does.
 template <class E, int THREADS, int UNROLL, bool SAME_PHASE>
-__global__ void __launch_bounds__(THREADS) distill_bwd_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const DistillParams p) {
   using S = typename E::storage;
   extern __shared__ uint4 distill_smem[];
   __shared__ float sh_factor, sh_x0;
@@ -357,78 +473,84 @@ __global__ void __launch_bounds__(THREADS) distill_bwd_kernel(const DistillParam
   const int64_t r = blockIdx.x;
   const int64_t b = r / p.x.L, l = r - b * p.x.L;
   const int tid = threadIdx.x, V = p.x.V, K = p.K;
+  const bool list_warp = tid >= THREADS;
   const bool live = p.mask == nullptr || p.mask[r] != 0;
   const float g = live ? p.dloss[r] / p.T : 0.f;
-  const float lse = p.lse[r], p_rest = p.p_rest[r];
   S* out = static_cast<S*>(p.dx.ptr) + b * p.dx.sb + l * p.dx.sl;
   const S* row = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
   const RowSplit sp = split_row<E>(out, V);
-  const Span sn = whole_row(sp);
   if (g == 0.f) {
-    fill_span<E, THREADS>(out, sp, sn, 0u);
+    if (!list_warp) fill_span<E, THREADS>(out, sp, whole_row(sp), 0u);
     return;
   }
-  Slots sl;
-  sl.id = reinterpret_cast<int*>(distill_smem);
-  sl.lq = reinterpret_cast<float*>(sl.id + K);
-  sl.x = sl.lq + K;
-  load_slots<E, THREADS>(sl, p, r, row);
-  __syncthreads();
-  if (tid < 32) {
+  const Slots sl = slots_at(distill_smem, K);
+  if (list_warp) {
+    const int lane = tid - THREADS;
+    const float lse = p.lse[r], p_rest = p.p_rest[r];
+    load_slots<E>(sl, p, r, row);
+    __syncwarp();
     const Teacher te = teacher_of(sl, K, p.tail);
     float S_sum = 0.f;
-    const double lse_d = static_cast<double>(lse);
-    for (int k = tid; k < K; k += 32) {
+    for (int k = lane; k < K; k += 32) {
       if (sl.id[k] < 0) continue;
-      const double lp = static_cast<double>(sl.x[k]) * p.invT - lse_d;
-      const double lq = static_cast<double>(sl.lq[k]) - te.shift;
-      const float pk = expf(static_cast<float>(lp));
-      const Term t = bucket(expf(static_cast<float>(lq)), pk, static_cast<float>(lq - lp), p.beta);
+      const Scaled z = over_T(sl.x[k], p);
+      const float lp = z.hi - lse, lq = sl.lq[k] - te.shift;  // lp: near lse, so the difference is exact
+      const float pk = expf(lp + z.lo);
+      const Term t = bucket(expf(lq), pk, pk == 0.f ? INFINITY : (lq - lp) - z.lo, p.beta);
       S_sum += t.G;
       sl.x[k] = pk;
       sl.lq[k] = t.G;
     }
-    const Term t = bucket(static_cast<float>(te.q_rest), p_rest, rest_ratio(te.q_rest, static_cast<double>(p_rest)),
-                          p.beta);
+    const Term t = bucket(te.rest, p_rest, rest_ratio(te.rest, p_rest, te.rest - p_rest), p.beta);
     S_sum = warp_sum(S_sum) + t.G;
-    for (int k = tid; k < K; k += 32) sl.lq[k] = g * (sl.lq[k] - sl.x[k] * S_sum);
+    for (int k = lane; k < K; k += 32) sl.lq[k] = g * (sl.lq[k] - sl.x[k] * S_sum);
     // p_j = 2^((x_j - x0) c) e^(x0 / T - lse): x0 takes up lse, so that no exponent is a small
     // difference of large products
-    if (tid == 0) {
-      const float x0 = static_cast<float>(lse_d * static_cast<double>(p.T));
-      const float scale = expf(static_cast<float>(static_cast<double>(x0) * p.invT - lse_d));
-      sh_factor = g * ((p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum) * scale;
+    if (lane == 0) {
+      const float x0 = lse * p.T;
+      const Scaled z = over_T(x0, p);
+      sh_factor = g * ((p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum) * expf((z.hi - lse) + z.lo);
       sh_x0 = x0;
     }
   }
   __syncthreads();
-  const float f = sh_factor;
-  if (f == 0.f) fill_span<E, THREADS>(out, sp, sn, 0u);
-  else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, sp, sh_x0, p.c, f);
+  if (!list_warp) {
+    const float f = sh_factor;
+    if (f == 0.f) fill_span<E, THREADS>(out, sp, whole_row(sp), 0u);
+    else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, sp, sh_x0, p.c, f);
+  }
   __syncthreads();  // the listed columns' values go over the stream's
-  for (int k = tid; k < K; k += THREADS)
-    if (sl.id[k] >= 0) E::store_scalar(out + sl.id[k], sl.lq[k]);
+  if (list_warp)
+    for (int k = tid - THREADS; k < K; k += 32)
+      if (sl.id[k] >= 0) E::store_scalar(out + sl.id[k], sl.lq[k]);
 }
 
-template <class E, int THREADS, int U>
-cudaError_t launch_distill_fwd_t(const DistillParams& p, int64_t rows, cudaStream_t s) {
+template <class E, int THREADS, int U, bool FUSED, bool SAME_PHASE>
+cudaError_t launch_distill_k(const DistillParams& p, int64_t rows, int keep_bytes, cudaStream_t s) {
   const int bm = bitmap_bytes<E>(p.x.V);
-  return launch_after_previous_smem(distill_fwd_kernel<E, THREADS, U>, dim3(static_cast<unsigned>(rows)),
-                                    dim3(THREADS), static_cast<size_t>(bm) + 12 * p.K, s, p, bm);
+  const size_t smem = static_cast<size_t>(keep_bytes) + bm + 12 * static_cast<size_t>(p.K);
+  if (smem > 46 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(distill_kernel<E, THREADS, U, FUSED, SAME_PHASE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kFusedKeepBytes + kBitmapBytes + 12 * kDistillMaxK);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after_previous_smem(distill_kernel<E, THREADS, U, FUSED, SAME_PHASE>,
+                                    dim3(static_cast<unsigned>(rows)), dim3(THREADS + 32), smem, s, p, bm,
+                                    keep_bytes / 16);
 }
 
 template <class E>
 cudaError_t launch_distill_fwd_e(const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
-  switch (pick_threads_fwd(p.x.V, sizeof(typename E::storage), rows, sms)) {
-    case 64: return launch_distill_fwd_t<E, 64, kUnroll>(p, rows, s);
-    case 128: return launch_distill_fwd_t<E, 128, 2>(p, rows, s);
-    default: return launch_distill_fwd_t<E, 256, kUnroll>(p, rows, s);
-  }
+  (void)sms;
+  return static_cast<int64_t>(p.x.V) * sizeof(typename E::storage) <= 8192
+             ? launch_distill_k<E, 64, kUnroll, false, true>(p, rows, 0, s)
+             : launch_distill_k<E, 256, kUnroll, false, true>(p, rows, 0, s);
 }
 
 template <class E, int THREADS>
 cudaError_t launch_distill_bwd_t(bool same_phase, const DistillParams& p, int64_t rows, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(rows)), block(THREADS);
+  const dim3 grid(static_cast<unsigned>(rows)), block(THREADS + 32);
   const size_t smem = 12 * static_cast<size_t>(p.K);
   return same_phase ? launch_after_previous_smem(distill_bwd_kernel<E, THREADS, kUnroll, true>, grid, block, smem, s, p)
                     : launch_after_previous_smem(distill_bwd_kernel<E, THREADS, kUnroll, false>, grid, block, smem, s,
@@ -440,6 +562,24 @@ cudaError_t launch_distill_bwd_e(bool same_phase, const DistillParams& p, int64_
   return pick_threads_bwd(p.x.V, sizeof(typename E::storage), rows, sms) == 64
              ? launch_distill_bwd_t<E, 64>(same_phase, p, rows, s)
              : launch_distill_bwd_t<E, 256>(same_phase, p, rows, s);
+}
+
+template <class E, int THREADS>
+cudaError_t launch_distill_fused_t(bool same_phase, const DistillParams& p, int64_t rows, int keep, cudaStream_t s) {
+  return same_phase ? launch_distill_k<E, THREADS, kUnroll, true, true>(p, rows, keep, s)
+                    : launch_distill_k<E, THREADS, kUnroll, true, false>(p, rows, 0, s);
+}
+
+// Thread counts and the part of long rows that is kept: as for grpo_loss_fused (the keep less
+// the bitmap and the list, so that two CTAs still share an SM).
+template <class E>
+cudaError_t launch_distill_fused_e(bool same_phase, const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
+  (void)sms;
+  const int64_t bytes = static_cast<int64_t>(p.x.V) * sizeof(typename E::storage);
+  if (bytes <= 8192) return launch_distill_fused_t<E, 64>(same_phase, p, rows, 0, s);
+  if (bytes < 131072) return launch_distill_fused_t<E, 256>(same_phase, p, rows, 0, s);
+  const int keep = (kFusedKeepBytes - bitmap_bytes<E>(p.x.V) - 12 * p.K) / 1024 * 1024;
+  return launch_distill_fused_t<E, 512>(same_phase, p, rows, keep, s);
 }
 
 }  // namespace
