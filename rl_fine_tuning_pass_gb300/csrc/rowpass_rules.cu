@@ -18,6 +18,7 @@
 // stream nearly every warp met one, and its 32 lanes waited for it (1.24 ms against DUAL ms for
 // forward and backward at (4, 1024, 151936) bf16).  Values are formed in fp32 from the whole count
 // and rounded once.
+#include "logits_load.cuh"
 #include "logits_ops.h"
 #include "rowpass_common.cuh"
 
@@ -68,15 +69,6 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* m, int j, int words)
   const int w = j >> 5;
   const uint32_t hi = w + 1 < words ? m[w + 1] : 0u;
   return __funnelshift_r(m[w], hi, j & 31);
-}
-
-template <class E>
-__device__ __forceinline__ uint4 load_any(const typename E::storage* body, int i, bool same_phase) {
-  if (same_phase) return ld_v4(reinterpret_cast<const uint4*>(body) + i);
-  float f[E::kVec];
-#pragma unroll
-  for (int q = 0; q < E::kVec; ++q) f[q] = E::load_scalar_coherent(body + static_cast<int64_t>(i) * E::kVec + q);
-  return E::pack(f, 0u);
 }
 
 // Grid: tiles x runs, tiles innermost.  run: rows per CTA, runs: runs per sequence.
@@ -188,6 +180,10 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
     __syncthreads();
   }
 
+  // the output may be the input where they are in phase
+  auto load = [&](const S* body, int i, int nvec) {
+    return same_phase ? ld_v4(reinterpret_cast<const uint4*>(body) + i) : load_out_of_phase<E>(body, i, nvec);
+  };
   constexpr uint32_t kAll = (1u << VEC) - 1u;
   constexpr uint32_t kForbidden = BWD ? 0u : (sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u);  // 0 or -inf
   for (int rr = 0; rr < nrows; ++rr) {
@@ -217,7 +213,7 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int i = i0 + tid + k * kRulesThreads;
-      if (i < i1 && !none(k) && !(INPLACE && full(k))) v[k] = load_any<E>(src + sp.head, i, same_phase);
+      if (i < i1 && !none(k) && !(INPLACE && full(k))) v[k] = load(src + sp.head, i, sp.nvec);
     }
 
     if (used) {
