@@ -30,7 +30,7 @@ constexpr int kTileVecs = 1024;  // vectors of a row per CTA, 4 per thread
 constexpr int kPer = kTileVecs / kRulesThreads;
 constexpr int kMaxRun = 32;      // rows per CTA
 constexpr int kWindow = 256;     // tokens past the first row's history that are held ready
-constexpr int kListed = 2048;    // touched columns that are listed; with more, the bitmap is searched
+constexpr int kListed = 2048;    // touched columns that are listed; with more, the words are searched
 
 struct SeqRules {
   float rho, freq, pres;
@@ -47,6 +47,10 @@ __device__ __forceinline__ float apply_rules(const SeqRules& q, float x, uint32_
   const uint32_t at = w >> kRuleBiasShift;
   if (at != 0) x += q.bias[at - 1];
   return x;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int k) {
+  return k == 0 ? v.x : (k == 1 ? v.y : (k == 2 ? v.z : v.w));
 }
 
 // `fill` (a pair of equal elements, or one fp32) where ok's bit is 0.
@@ -77,10 +81,9 @@ template <class E, bool BWD, bool INPLACE>
 __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesParams p, int tiles, int run, int runs,
                                                                  bool same_phase) {
   constexpr int VEC = E::kVec, W = kTileVecs * VEC, COLS = W + VEC;  // a tile's last vector may reach past it
-  constexpr int MAPW = (COLS + 31) / 32;
+  constexpr int WORDS = BWD ? (COLS + 127) / 128 * 4 : (COLS + 3) / 4 * 4;
   using S = typename E::storage;
-  extern __shared__ uint4 rules_smem[];  // words, one per column (forward)
-  __shared__ uint32_t touched[MAPW];
+  extern __shared__ uint4 rules_smem[];  // forward: a word per column; backward: a bit
   __shared__ uint16_t listed[kListed];
   __shared__ int sh_touched;
   __shared__ int sh_len[kMaxRun];
@@ -112,31 +115,27 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
   auto bad_index = [&]() {
     if (p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
   };
-  auto touch = [&](int col) {
-    const uint32_t bit = 1u << (col & 31);
-    if (atomicOr(&touched[col >> 5], bit) & bit) return;
+  auto add_token = [&](int col, int i) {  // column col of the tile, place i of the history
+    if (BWD) atomicOr(&words[col >> 5], 1u << (col & 31));
+    else if (i < np) atomicOr(&words[col], kRulePrompt);
+    else atomicAdd(&words[col], 1u);
+  };
+  auto is_touched = [&](int col) { return BWD ? (words[col >> 5] >> (col & 31) & 1u) != 0 : words[col] != 0u; };
+  auto list = [&](int col) {
     const int at = atomicAdd(&sh_touched, 1);
     if (at < kListed) listed[at] = static_cast<uint16_t>(col);
   };
-  auto add_token = [&](int col, int i) {  // column col of the tile, place i of the history
-    if (!BWD) {
-      if (i < np) atomicOr(&words[col], kRulePrompt);
-      else atomicAdd(&words[col], 1u);
-    }
-    touch(col);
-  };
   // the tile's column of a token, -1 where it has none, -2 past the vocabulary
   auto col_of = [&](int64_t id) {
-    const int64_t col = id - c0;
-    return id >= V ? -2 : (id >= 0 && col >= 0 && col < COLS ? static_cast<int>(col) : -1);
+    if (static_cast<uint64_t>(id) >= static_cast<uint64_t>(V)) return id < 0 ? -1 : -2;
+    const int col = static_cast<int>(id) - c0;
+    return static_cast<unsigned>(col) < static_cast<unsigned>(COLS) ? col : -1;
   };
   int held = 0;  // the words hold the history's first `held` tokens; the window what follows `win`
   int win = 0;
   auto rebuild = [&](int n) {  // count the first n tokens
     __syncthreads();
-    if (!BWD)
-      for (int i = tid; i < (COLS + 3) / 4; i += kRulesThreads) rules_smem[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < MAPW; i += kRulesThreads) touched[i] = 0u;
+    for (int i = tid; i < WORDS / 4; i += kRulesThreads) rules_smem[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) sh_touched = 0;
     __syncthreads();
     if (biased) {
@@ -146,7 +145,6 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
         if (col < 0) continue;
         // a column listed twice: the last entry counts
         atomicMax(&words[col], static_cast<uint32_t>(m + 1) << kRuleBiasShift);
-        touch(col);
       }
       __syncthreads();
     }
@@ -165,6 +163,20 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
       if (nrows > 1 && tid < kWindow && n + tid < N) window[tid] = col_of(tk[n + tid]);
     }
     held = win = n;
+    __syncthreads();
+    for (int i = tid; i < WORDS / 4; i += kRulesThreads) {
+      const uint4 v = rules_smem[i];
+      if ((v.x | v.y | v.z | v.w) == 0u) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w = word_of(v, k);
+        if (!BWD) {
+          if (w != 0u) list(4 * i + k);
+        } else {
+          for (; w != 0u; w &= w - 1u) list(32 * (4 * i + k) + __ffs(w) - 1);
+        }
+      }
+    }
     __syncthreads();
   };
 
@@ -226,7 +238,10 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
           if (col == -2) bad_index();
           if (col < 0) continue;
           __syncthreads();
-          if (tid == 0) add_token(col, held);
+          if (tid == 0) {
+            if (!is_touched(col)) list(col);
+            add_token(col, held);
+          }
           __syncthreads();
         }
       }
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(kRulesThreads, 5) rules_kernel(const RulesPara
     auto look = [&](int t) {
       Hit h{-1, t, 0.f, 0.f};
       if (nt <= kListed) h.col = listed[t];
-      else if ((touched[t >> 5] >> (t & 31) & 1u) == 0) return h;
+      else if (!is_touched(t)) return h;
       const int j = c0 + h.col;
       if (j >= V) return h;
       int first = j;  // the column that decides whose it is
@@ -301,8 +316,8 @@ cudaError_t launch_e(bool same_phase, const RulesParams& p, int64_t rows, int sm
   run = run < 1 ? 1 : (run > kMaxRun ? kMaxRun : run);
   if (run > p.x.L) run = p.x.L;
   const int64_t runs = (p.x.L + run - 1) / run;
-  const bool used = !BWD && (p.tokens != nullptr || p.M > 0);
-  constexpr int most = (COLS + 3) / 4 * 16;
+  const bool used = (p.tokens != nullptr && (!BWD || p.repetition != nullptr)) || (!BWD && p.M > 0);
+  constexpr int most = BWD ? (COLS + 127) / 128 * 16 : (COLS + 3) / 4 * 16;
   static_assert(most < 40 * 1024, "with the static part within the 48 KB that need no leave");
   const int64_t grid = rows / p.x.L * runs * tiles;
   return launch_after_previous_smem(rules_kernel<E, BWD, INPLACE>, dim3(static_cast<unsigned>(grid)),

@@ -3,19 +3,22 @@
 //
 // One sweep over the row forms the softmax statistic (logits_stat.cuh) and notes where
 // candidates are.  Each thread keeps the largest element it has met in the even and in the odd
-// places of its vectors, 512 maxima per CTA; the K-th largest of those maxima is a lower bound of
+// places of its vectors, 512 maxima per CTA (up to K = 64 one of both, 256); the K-th largest of those maxima is a lower bound of
 // the K-th largest element seen so far (K different elements reach it), so a chunk (the vectors of
 // one thread in one step) without an element that reaches it cannot hold a result.  The bound is
 // taken anew after 1, 2, 4, 8, ... steps of the sweep: of N(0, 1) elements about 64 chunks of the
 // first step reach it at K = 64, and as many of each doubling, some 330 of a row of 151936.  The
 // chunks that also reach the last bound (about 64) are read again, and their elements that reach
-// it (about 70) are ranked by counting.
+// it (about 70) are ranked by counting.  With few rows, where a CTA's
+// part is a few steps, all its chunks are noted and the bound is taken once, at the end.
 //
 // Rows that collect more than the buffers hold (thousands of ties at the K-th value, large
 // values that come last) are done again by radix selection on order-preserving keys.
 //
 // With few rows, a cluster of CTAs takes a row: each CTA ranks its own part, the first one
 // merges the sorted lists and the statistics, which the others write into its shared memory.
+#include <climits>
+
 #include "logits_ops.h"
 #include "logits_stat.cuh"
 
@@ -143,23 +146,37 @@ __device__ void radix_select(const typename E::storage* row, int V, int K, uint6
 }
 
 constexpr int kMaxima = 2 * kTopkThreads;   // running maxima per CTA
+constexpr int kOneMaximum = 64;             // up to this K one maximum per thread is enough
 constexpr int kSurvivors = 1024;            // entries ranked by counting
 constexpr uint32_t kKeyNegInf = 0x007Fu;    // high half of the key of -inf
 
-// High half of the K-th largest of the CTA's running maxima (keys in sh; warp 0 only).
+// A lower bound of the K-th largest of the CTA's running maxima (high halves of their keys in sh;
+// warp 0 only) that K of them or more reach: that key's high half, or, where just K reach a smaller
+// prefix of it, the prefix.
 __device__ __forceinline__ uint32_t kth_maximum(const uint16_t* sh, int K) {
+  constexpr int kPer = kTopkThreads / 32;
   const int lane = threadIdx.x;
-  uint32_t k[kMaxima / 32];
+  const bool two = K > kOneMaximum;
+  uint32_t k[2 * kPer];
 #pragma unroll
-  for (int q = 0; q < kMaxima / 32; ++q) k[q] = sh[lane + 32 * q];
+  for (int q = 0; q < kPer; ++q) {
+    k[q] = sh[lane + 32 * q];
+    k[kPer + q] = two ? sh[kTopkThreads + lane + 32 * q] : 0u;
+  }
   uint32_t best = 0u;
 #pragma unroll 1
   for (uint32_t bit = 0x8000u; bit != 0u; bit >>= 1) {
     const uint32_t cand = best | bit;
     int n = 0;
 #pragma unroll
-    for (int q = 0; q < kMaxima / 32; ++q) n += k[q] >= cand;
-    if (__reduce_add_sync(0xFFFFFFFFu, n) >= K) best = cand;
+    for (int q = 0; q < kPer; ++q) n += k[q] >= cand;
+    if (two) {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) n += k[kPer + q] >= cand;
+    }
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (n >= K) best = cand;
+    if (n == K) break;
   }
   return best;
 }
@@ -217,8 +234,12 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
 
   float thr = -INFINITY;
   auto bound = [&]() {  // a new bound from the maxima so far
-    maxima[tid] = static_cast<uint16_t>(key_of(sub.x) >> 16);
-    maxima[T + tid] = static_cast<uint16_t>(key_of(sub.y) >> 16);
+    if (K <= kOneMaximum) {
+      maxima[tid] = static_cast<uint16_t>(key_of(fmaxf(sub.x, sub.y)) >> 16);
+    } else {
+      maxima[tid] = static_cast<uint16_t>(key_of(sub.x) >> 16);
+      maxima[T + tid] = static_cast<uint16_t>(key_of(sub.y) >> 16);
+    }
     __syncthreads();
     if (tid < 32) {
       const uint32_t k = kth_maximum(maxima, K);
@@ -228,7 +249,8 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     thr = sh_thr;
   };
   const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
-  int step = 0, next = 1;
+  const bool all = CS > 1 && (v1 - v0 + U * T - 1) / (U * T) * T <= cap;  // every chunk fits
+  int step = 0, next = all ? INT_MAX : 1;
   auto fold = [&](const uint4 (&v)[U], int i) {
     const float2 pm = maxrun_vectors<E>(rs, v, c);
     sub.x = fmaxf(sub.x, pm.x);
@@ -238,7 +260,9 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
       next *= 2;
     }
     const float m = fmaxf(pm.x, pm.y);
-    if (m >= thr && m > -INFINITY) {
+    if (all) {
+      cand[(step - 1) * T + tid] = static_cast<uint64_t>(key_of(m)) << 32 | static_cast<uint32_t>(i);
+    } else if (m >= thr && m > -INFINITY) {
       const unsigned at = atomicAdd(&sh_n, 1u);
       if (at < static_cast<unsigned>(cap)) cand[at] = static_cast<uint64_t>(key_of(m)) << 32 | static_cast<uint32_t>(i);
     }
@@ -260,12 +284,12 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     }
     fold(v, i0 + tid);
   }
-  if (step * 2 != next) bound();  // elements since the last bound
+  if (all || step * 2 != next) bound();  // elements since the last bound
   MaxStat st = maxstat_block<T>(rs.stat(), c);
   __syncthreads();
 
   // the elements of the noted chunks that reach the last bound: four threads to a chunk
-  const unsigned n = sh_n;
+  const unsigned n = all ? static_cast<unsigned>(step * T) : sh_n;
   const uint32_t least = key_of(thr);
   if (edge > -INFINITY && edge >= thr) take(edge, edge_j);
   for (unsigned q = tid; q < U * min(n, static_cast<unsigned>(cap)); q += T) {
