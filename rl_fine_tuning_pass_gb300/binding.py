@@ -634,7 +634,8 @@ def distill_topk_fwd(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, 
     x, B, L, _ = _pack_rows(logits)
     R, dev = B * L, logits.device
     pi, pt, K = _list_of(ids, teacher_logp, R, dev)
-    loss, lse, p_rest = torch.empty((3, R), dtype=torch.float32, device=dev).unbind(0)
+    loss = torch.empty(R, dtype=torch.float32, device=dev)
+    lse, p_rest = torch.empty_like(loss), torch.empty_like(loss)
     _call("distill_topk_fwd", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev), T, beta, bool(tail),
           loss.data_ptr(), lse.data_ptr(), p_rest.data_ptr(), _on(dev_err, torch.int32, 1, "dev_err", dev))
     return {"loss": loss, "lse": lse, "p_rest": p_rest}
@@ -663,7 +664,8 @@ def distill_topk_fused(logits, ids, teacher_logp, dloss, *, T=1.0, beta=0.0, tai
     R, dev = B * L, logits.device
     dlogits, dx = _like(dlogits, logits, "dlogits")
     pi, pt, K = _list_of(ids, teacher_logp, R, dev)
-    loss, lse, p_rest = torch.empty((3, R), dtype=torch.float32, device=dev).unbind(0)
+    loss = torch.empty(R, dtype=torch.float32, device=dev)
+    lse, p_rest = torch.empty_like(loss), torch.empty_like(loss)
     _call("distill_topk_fused", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
           _on(dloss, torch.float32, R, "dloss", dev), T, beta, bool(tail), loss.data_ptr(), lse.data_ptr(),
           p_rest.data_ptr(), dx, _on(dev_err, torch.int32, 1, "dev_err", dev))
