@@ -311,13 +311,27 @@ __device__ __forceinline__ void grad_stream(const typename E::storage* in, typen
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k) process(v[k], i + k * THREADS);
     }
-    for (; i < n; i += THREADS) process(load(i), i);
+    if (i < n) {  // the last step: its loads go out together too
+      uint4 v[UNROLL];
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k)
+        if (i + k * THREADS < n) v[k] = load(i + k * THREADS);
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k)
+        if (i + k * THREADS < n) process(v[k], i + k * THREADS);
+    }
   };
-  auto load = [&](int j) {
-    if constexpr (SAME_PHASE) return ld_v4_evict_first(reinterpret_cast<const uint4*>(ib) + j);
-    else return load_out_of_phase<E>(ib, j, sp.nvec);
-  };
-  sweep(load, kept_vecs + tid, sp.nvec);
+  if constexpr (SAME_PHASE) {
+    sweep([&](int j) { return ld_v4_evict_first(reinterpret_cast<const uint4*>(ib) + j); }, kept_vecs + tid, sp.nvec);
+  } else {
+    for (int i = tid; i < sp.nvec; i += UNROLL * THREADS) {
+      uint4 v[UNROLL];
+      load_out_of_phase<E, UNROLL, THREADS>(v, ib, i, sp.nvec, sp.nvec);
+#pragma unroll
+      for (int k = 0; k < UNROLL; ++k)
+        if (i + k * THREADS < sp.nvec) process(v[k], i + k * THREADS);
+    }
+  }
   if (kept_vecs > 0) sweep([&](int j) { return kept[j]; }, tid, kept_vecs);
 }
 
@@ -412,9 +426,17 @@ __global__ void __launch_bounds__(THREADS + 32) distill_kernel(const DistillPara
         for (int k = 0; k < UNROLL; ++k) leave_out(v[k], i + k * THREADS);
         maxrun_vectors<E>(rs, v, c);
       }
-      for (; i < n; i += THREADS) {
-        uint4 v[1] = {load(i)};
-        leave_out(v[0], i);
+      if (i < n) {  // the last step: its loads go out together too
+        const uint32_t pad = sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+        uint4 v[UNROLL];
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {
+          v[k] = make_uint4(pad, pad, pad, pad);
+          if (i + k * THREADS < n) v[k] = load(i + k * THREADS);
+        }
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k)
+          if (i + k * THREADS < n) leave_out(v[k], i + k * THREADS);
         maxrun_vectors<E>(rs, v, c);
       }
     };
@@ -489,6 +511,10 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
     return;
   }
   const Slots sl = slots_at(distill_smem, K);
+  // long rows: their start comes to L2 while the list is worked on (999 rows of 200 KB: 64 us against
+  // 67 us; rows of 64 KB took longer with it)
+  const int64_t row_bytes = static_cast<int64_t>(V) * sizeof(S);
+  if (tid == 0 && row_bytes >= 131072) prefetch_row(row, row_bytes);
   if (list_warp) {
     const int lane = tid - THREADS;
     const float lse = p.lse[r], p_rest = p.p_rest[r];
@@ -545,50 +571,54 @@ cudaError_t launch_distill_k(const DistillParams& p, int64_t rows, int keep_byte
                                     keep_bytes / 16);
 }
 
-// Streaming threads of the forward: 64 for short rows; 128 where that lets every row be resident at
-// once (7 such CTAs per SM; 999 rows of 200 KB, forward + backward: 94 us against 107 us with 256
-// threads); else 256 (8192 rows of 304 KB: 998 us against 1057 us with 128).
+// Streaming threads of the forward, and vectors in flight of each: 64 x 4 for short rows; 128 x 8 while
+// that leaves most rows resident (7 such CTAs per SM: 2048 rows of 64 KB 26 us, against 30 us with
+// 256 x 4 and 34 us with 256 x 8, whose last step is mostly empty); else 256 x 4.
 template <class E>
 cudaError_t launch_distill_fwd_e(const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
   if (static_cast<int64_t>(p.x.V) * sizeof(typename E::storage) <= 8192)
     return launch_distill_k<E, 64, kUnroll, false, true>(p, rows, 0, s);
-  return rows <= 7LL * sms ? launch_distill_k<E, 128, kUnroll, false, true>(p, rows, 0, s)
-                           : launch_distill_k<E, 256, kUnroll, false, true>(p, rows, 0, s);
+  return rows <= 20LL * sms ? launch_distill_k<E, 128, 8, false, true>(p, rows, 0, s)
+                            : launch_distill_k<E, 256, kUnroll, false, true>(p, rows, 0, s);
 }
 
-template <class E, int THREADS>
+template <class E, int THREADS, int U>
 cudaError_t launch_distill_bwd_t(bool same_phase, const DistillParams& p, int64_t rows, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(rows)), block(THREADS + 32);
   const size_t smem = 12 * static_cast<size_t>(p.K);
-  return same_phase ? launch_after_previous_smem(distill_bwd_kernel<E, THREADS, kUnroll, true>, grid, block, smem, s, p)
+  return same_phase ? launch_after_previous_smem(distill_bwd_kernel<E, THREADS, U, true>, grid, block, smem, s, p)
                     : launch_after_previous_smem(distill_bwd_kernel<E, THREADS, kUnroll, false>, grid, block, smem, s,
                                                  p);
 }
 
+// Long rows with eight vectors in flight per thread (8192 rows of 304 KB: 662 us against 673 us).
 template <class E>
 cudaError_t launch_distill_bwd_e(bool same_phase, const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
-  return pick_threads_bwd(p.x.V, sizeof(typename E::storage), rows, sms) == 64
-             ? launch_distill_bwd_t<E, 64>(same_phase, p, rows, s)
-             : launch_distill_bwd_t<E, 256>(same_phase, p, rows, s);
+  const int64_t bytes = static_cast<int64_t>(p.x.V) * sizeof(typename E::storage);
+  if (pick_threads_bwd(p.x.V, sizeof(typename E::storage), rows, sms) == 64)
+    return launch_distill_bwd_t<E, 64, kUnroll>(same_phase, p, rows, s);
+  return bytes < 131072 ? launch_distill_bwd_t<E, 256, kUnroll>(same_phase, p, rows, s)
+                        : launch_distill_bwd_t<E, 256, 8>(same_phase, p, rows, s);
 }
 
-template <class E, int THREADS>
+template <class E, int THREADS, int U>
 cudaError_t launch_distill_fused_t(bool same_phase, const DistillParams& p, int64_t rows, int keep, cudaStream_t s) {
-  return same_phase ? launch_distill_k<E, THREADS, kUnroll, true, true>(p, rows, keep, s)
+  return same_phase ? launch_distill_k<E, THREADS, U, true, true>(p, rows, keep, s)
                     : launch_distill_k<E, THREADS, kUnroll, true, false>(p, rows, 0, s);
 }
 
 // The part of long rows that is kept is that of grpo_loss_fused less the bitmap and the list, so that
-// two CTAs still share an SM.  Shorter rows: 128 streaming threads (2048 rows of 64 KB: 55 us against
-// 61 us with 256: more CTAs are in different phases of their rows).
+// two CTAs still share an SM.  Shorter rows: 128 streaming threads, eight vectors in flight each (2048
+// rows of 64 KB: 51 us; 58 us with four in flight, 61 us with 256 x 4: more CTAs are in different phases
+// of their rows).
 template <class E>
 cudaError_t launch_distill_fused_e(bool same_phase, const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
   (void)sms;
   const int64_t bytes = static_cast<int64_t>(p.x.V) * sizeof(typename E::storage);
-  if (bytes <= 8192) return launch_distill_fused_t<E, 64>(same_phase, p, rows, 0, s);
-  if (bytes < 131072) return launch_distill_fused_t<E, 128>(same_phase, p, rows, 0, s);
+  if (bytes <= 8192) return launch_distill_fused_t<E, 64, kUnroll>(same_phase, p, rows, 0, s);
+  if (bytes < 131072) return launch_distill_fused_t<E, 128, 8>(same_phase, p, rows, 0, s);
   const int keep = (kFusedKeepBytes - bitmap_bytes<E>(p.x.V) - 12 * p.K) / 1024 * 1024;
-  return launch_distill_fused_t<E, 512>(same_phase, p, rows, keep, s);
+  return launch_distill_fused_t<E, 512, kUnroll>(same_phase, p, rows, keep, s);
 }
 
 }  // namespace

@@ -33,7 +33,7 @@ constexpr int kRulesThreads = 256;
 constexpr int kTileVecs = 1024;  // vectors of a row per CTA, 4 per thread
 constexpr int kPer = kTileVecs / kRulesThreads;
 constexpr int kMaxRun = 8;       // rows per CTA
-constexpr int kBulkRun = 4;      // rows per CTA from which the bulk kernel is taken
+constexpr int kBulkRun = 4;      // rows per CTA from which the forward takes the bulk kernel
 constexpr int kWindow = 256;     // tokens past the first row's history that are held ready
 constexpr int kListed = 2048;    // touched columns that are listed; with more, the words are searched
 
@@ -301,10 +301,15 @@ __device__ __forceinline__ int edge_of(const Part& t, int V, int c0, int W) {
 }
 
 // Grid: tiles x runs, tiles innermost.  run: rows per CTA, runs: runs per sequence.
-// INPLACE: the output is the input, so only what changes is read and written.
-template <class E, bool BWD, bool INPLACE>
-__global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesParams p, int tiles, int run, int runs,
-                                                                 bool same_phase) {
+// HOW: the input and output rows.
+enum RulesHow : int {
+  kInPlace = 0,     // the same memory: only what changes is read and written
+  kInPhase = 1,     // equal addresses mod 16
+  kOutOfPhase = 2,  // others
+};
+template <class E, bool BWD, int HOW>
+__global__ void __launch_bounds__(kRulesThreads, BWD ? 4 : 3) rules_kernel(const RulesParams p, int tiles, int run, int runs) {
+  constexpr bool INPLACE = HOW == kInPlace;
   using H = History<E, BWD>;
   using S = typename E::storage;
   constexpr int VEC = E::kVec, W = H::W;
@@ -320,10 +325,6 @@ __global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesPara
   const int V = p.x.V, mwords = (V + 31) >> 5;
   H h(p, sh, reinterpret_cast<uint32_t*>(rules_smem), b, l0, nrows, c0);
 
-  // the output may be the input where they are in phase
-  auto load = [&](const S* body, int i, int nvec) {
-    return same_phase ? ld_v4(reinterpret_cast<const uint4*>(body) + i) : load_out_of_phase<E>(body, i, nvec);
-  };
   constexpr uint32_t kAll = (1u << VEC) - 1u;
   constexpr uint32_t kForbidden = BWD ? 0u : (sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u);  // 0 or -inf
   for (int rr = 0; rr < nrows; ++rr) {
@@ -337,6 +338,9 @@ __global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesPara
     const int i0 = part.i0, i1 = part.i1;
 
     // the vectors, and which of their columns are allowed (a byte each)
+    uint4 v[kPer];
+    if constexpr (HOW == kOutOfPhase)
+      load_out_of_phase<E, kPer, kRulesThreads>(v, src + sp.head, i0 + tid, i1, sp.nvec);
     uint32_t allowed = 0xFFFFFFFFu;
     if (m != nullptr) {
 #pragma unroll
@@ -347,11 +351,12 @@ __global__ void __launch_bounds__(kRulesThreads, 4) rules_kernel(const RulesPara
     }
     auto full = [&](int k) { return (allowed >> (8 * k) & kAll) == kAll; };
     auto none = [&](int k) { return (allowed >> (8 * k) & kAll) == 0u; };
-    uint4 v[kPer];
+    if constexpr (HOW != kOutOfPhase) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int i = i0 + tid + k * kRulesThreads;
-      if (i < i1 && !none(k) && !(INPLACE && full(k))) v[k] = load(src + sp.head, i, sp.nvec);
+      for (int k = 0; k < kPer; ++k) {
+        const int i = i0 + tid + k * kRulesThreads;
+        if (i < i1 && !none(k) && !(INPLACE && full(k))) v[k] = ld_v4(reinterpret_cast<const uint4*>(src + sp.head) + i);
+      }
     }
     h.go_to(rr);
 
@@ -522,45 +527,43 @@ int64_t pick_run(int64_t rows, int64_t L, int tiles, int64_t places) {
   return run < L ? run : L;
 }
 
-template <class E, bool BWD, bool INPLACE>
-cudaError_t launch_e(bool same_phase, const RulesParams& p, int64_t rows, int sms, cudaStream_t s) {
+template <class E, bool BWD, int HOW>
+cudaError_t launch_e(const RulesParams& p, int64_t rows, int sms, cudaStream_t s) {
   using H = History<E, BWD>;
   const int tiles = (p.x.V + H::W - 1) / H::W;
   const bool used = (p.tokens != nullptr && (!BWD || p.repetition != nullptr)) || (!BWD && p.M > 0);
   const int words = used ? H::WORDS * 4 : 0;
   static_assert(H::WORDS * 4 < 40 * 1024, "with the static part within the 48 KB that need no leave");
-  const int64_t run = pick_run(rows, p.x.L, tiles, 4LL * sms);
-  if (!INPLACE && same_phase && p.allowed == nullptr && run >= kBulkRun) {
-    constexpr int ring = kStagesOf<BWD> * kTileVecs * 16, most = ring + H::WORDS * 4;
-    const cudaError_t e =
-        cudaFuncSetAttribute(rules_bulk_kernel<E, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return e;
-    const int64_t runs = (p.x.L + run - 1) / run;
-    return launch_after_previous_smem(rules_bulk_kernel<E, BWD>, dim3(static_cast<unsigned>(rows / p.x.L * runs * tiles)),
-                                      dim3(kRulesThreads), ring + words, s, p, tiles,
-                                      static_cast<int>(run), static_cast<int>(runs));
+  const int64_t run = pick_run(rows, p.x.L, tiles, 4LL * sms), runs = (p.x.L + run - 1) / run;
+  const dim3 grid(static_cast<unsigned>(rows / p.x.L * runs * tiles)), block(kRulesThreads);
+  if constexpr (HOW == kInPhase) {
+    if (p.allowed == nullptr && (BWD || run >= kBulkRun)) {
+      constexpr int ring = kStagesOf<BWD> * kTileVecs * 16, most = ring + H::WORDS * 4;
+      const cudaError_t e =
+          cudaFuncSetAttribute(rules_bulk_kernel<E, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (e != cudaSuccess) return e;
+      return launch_after_previous_smem(rules_bulk_kernel<E, BWD>, grid, block, ring + words, s, p, tiles,
+                                        static_cast<int>(run), static_cast<int>(runs));
+    }
   }
-  const int64_t runs = (p.x.L + run - 1) / run;
-  return launch_after_previous_smem(rules_kernel<E, BWD, INPLACE>, dim3(static_cast<unsigned>(rows / p.x.L * runs * tiles)),
-                                    dim3(kRulesThreads), words, s, p, tiles, static_cast<int>(run),
-                                    static_cast<int>(runs), same_phase);
+  return launch_after_previous_smem(rules_kernel<E, BWD, HOW>, grid, block, words, s, p, tiles, static_cast<int>(run),
+                                    static_cast<int>(runs));
 }
 
-template <class E>
-cudaError_t launch_d(bool bwd, bool same_phase, bool in_place, const RulesParams& p, int64_t rows, int sms,
-                     cudaStream_t s) {
-  if (bwd) return in_place ? launch_e<E, true, true>(same_phase, p, rows, sms, s)
-                           : launch_e<E, true, false>(same_phase, p, rows, sms, s);
-  return in_place ? launch_e<E, false, true>(same_phase, p, rows, sms, s)
-                  : launch_e<E, false, false>(same_phase, p, rows, sms, s);
+template <class E, bool BWD>
+cudaError_t launch_d(bool same_phase, bool in_place, const RulesParams& p, int64_t rows, int sms, cudaStream_t s) {
+  if (in_place) return launch_e<E, BWD, kInPlace>(p, rows, sms, s);
+  return same_phase ? launch_e<E, BWD, kInPhase>(p, rows, sms, s) : launch_e<E, BWD, kOutOfPhase>(p, rows, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rules(int dtype, bool bwd, bool same_phase, bool in_place, const RulesParams& p, int64_t rows,
                          int sms, cudaStream_t stream) {
-  return dtype == 1 ? launch_d<BF16>(bwd, same_phase, in_place, p, rows, sms, stream)
-                    : launch_d<F32>(bwd, same_phase, in_place, p, rows, sms, stream);
+  if (dtype == 1) return bwd ? launch_d<BF16, true>(same_phase, in_place, p, rows, sms, stream)
+                             : launch_d<BF16, false>(same_phase, in_place, p, rows, sms, stream);
+  return bwd ? launch_d<F32, true>(same_phase, in_place, p, rows, sms, stream)
+             : launch_d<F32, false>(same_phase, in_place, p, rows, sms, stream);
 }
 
 }  // namespace grpo

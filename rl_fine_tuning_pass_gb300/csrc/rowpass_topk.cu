@@ -6,8 +6,10 @@
 // places of its vectors, 512 maxima per CTA (up to K = 64 one of both, 256); the K-th largest of those maxima is a lower bound of
 // the K-th largest element seen so far (K different elements reach it), so a chunk (the vectors of
 // one thread in one step) without an element that reaches it cannot hold a result.  The bound is
-// taken anew after 1, 2, 4, 8, ... steps of the sweep: of N(0, 1) elements about 64 chunks of the
-// first step reach it at K = 64, and as many of each doubling, some 330 of a row of 151936.  The
+// taken anew after 1, 4, 16, ... steps of the sweep and at its end: of N(0, 1) elements about 64
+// chunks of the first step reach it at K = 64, and three times as many of each quadrupling, some 460
+// of a row of 151936 (a bound after each doubling notes fewer chunks and waits at more barriers:
+// 2048 rows of 32000 at K = 128 took 62 us, against 59 us).  The
 // chunks that also reach the last bound (about 64) are read again, and their elements that reach
 // it (about 70) are ranked by counting.  With few rows, where a CTA's
 // part is a few steps, all its chunks are noted and the bound is taken once, at the end.
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     sub.y = fmaxf(sub.y, pm.y);
     if (++step == next) {
       bound();
-      next *= 2;
+      next *= 4;
     }
     const float m = fmaxf(pm.x, pm.y);
     if (all) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     }
     fold(v, i0 + tid);
   }
-  if (all || step * 2 != next) bound();  // elements since the last bound
+  if (all || step * 4 != next) bound();  // elements since the last bound
   MaxStat st = maxstat_block<T>(rs.stat(), c);
   __syncthreads();
 
