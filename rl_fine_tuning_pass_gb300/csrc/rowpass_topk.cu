@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   __shared__ uint64_t list[kTopkMax];
   __shared__ TopkPart parts[CS];
   __shared__ float sh_thr;
-  __shared__ unsigned sh_n, sh_m;
+  __shared__ unsigned sh_n, sh_m, sh_c;
   uint64_t* cand = topk_smem;  // chunks: the largest element's key, and the first vector
   uint64_t* surv = topk_smem + cap;
   uint64_t* lists = surv + kSurvivors;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   const RowSplit sp = split_row<E>(row, V);
   const int part = (sp.nvec + CS - 1) / CS;
   const int v0 = min(sp.nvec, static_cast<int>(rank) * part), v1 = min(sp.nvec, v0 + part);
-  if (tid == 0) sh_n = sh_m = 0u;
+  if (tid == 0) sh_n = sh_m = sh_c = 0u;
   __syncthreads();
 
   MaxRun rs;
@@ -274,6 +274,10 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     uint4 v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) v[k] = ld_nc_v4(vb + i0 + k * T + tid);
+    if (tid == 0 && i0 + U * T < v1)  // ask L2 for the next step (8192 rows of 304 KB: 445 us against 462 us)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(vb + i0 + U * T),
+                   "r"(static_cast<uint32_t>(min(v1 - i0 - U * T, U * T)) * 16u)
+                   : "memory");
     fold(v, i0 + tid);
   }
   if (i0 < v1) {
@@ -290,14 +294,23 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   MaxStat st = maxstat_block<T>(rs.stat(), c);
   __syncthreads();
 
-  // the elements of the noted chunks that reach the last bound: four threads to a chunk
+  // the noted chunks that reach the last bound, then their elements that do, four threads to a chunk
   const unsigned n = all ? static_cast<unsigned>(step * T) : sh_n;
   const uint32_t least = key_of(thr);
+  constexpr unsigned kChunks = 2 * kTopkMax;
+  uint32_t* chunks = reinterpret_cast<uint32_t*>(list);
+  for (unsigned q = tid; q < min(n, static_cast<unsigned>(cap)); q += T) {
+    const uint64_t e = cand[q];
+    if (static_cast<uint32_t>(e >> 32) < least) continue;
+    const unsigned at = atomicAdd(&sh_c, 1u);
+    if (at < kChunks) chunks[at] = static_cast<uint32_t>(e);
+  }
+  __syncthreads();
+  const unsigned nc = sh_c;
   if (edge > -INFINITY && edge >= thr) take(edge, edge_j);
-  for (unsigned q = tid; q < U * min(n, static_cast<unsigned>(cap)); q += T) {
-    const uint64_t e = cand[q / U];
-    const int i = static_cast<int>(static_cast<uint32_t>(e)) + static_cast<int>(q % U) * T;
-    if (static_cast<uint32_t>(e >> 32) < least || i >= v1) continue;
+  for (unsigned q = tid; q < U * min(nc, kChunks); q += T) {
+    const int i = static_cast<int>(chunks[q / U]) + static_cast<int>(q % U) * T;
+    if (i >= v1) continue;
     float f[VEC];
     E::unpack(ld_nc_v4(vb + i), f);
 #pragma unroll
@@ -306,7 +319,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   }
   __syncthreads();
   int m = static_cast<int>(sh_m);
-  const bool over = n > static_cast<unsigned>(cap) || m > kSurvivors;
+  const bool over = n > static_cast<unsigned>(cap) || nc > kChunks || m > kSurvivors;
   uint64_t* mine = list;
   if (CS > 1) {
     cluster_wait();
