@@ -77,8 +77,8 @@ typedef enum { GRPO_FP32 = 0, GRPO_BF16 = 1 } grpo_dtype;
 /* Bits OR-ed into *dev_err by the kernels. */
 #define GRPO_DEVERR_IDX_OUT_OF_RANGE 1
 /* A kernel gave up waiting for its own asynchronous copies (about 2 s): a tensor-core GEMM of
- * grpo_fused_linear(_noalloc) (copies or MMAs), or a row of grpo_loss_fused (the bulk copy of
- * the part of the row kept in shared memory).  Those outputs are not valid.  The kernel
+ * grpo_fused_linear(_noalloc) (copies or MMAs), a row of grpo_loss_fused or distill_topk_fused
+ * (the bulk copy of the part of the row kept in shared memory), or a row of process_logits_*.  Those outputs are not valid.  The kernel
  * returns without trapping (the GEMM with its TMEM freed). */
 #define GRPO_DEVERR_TIMEOUT 2
 /* A row's list of teacher ids holds a column twice (distill_topk_*). */

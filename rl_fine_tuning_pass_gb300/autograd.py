@@ -100,18 +100,21 @@ class ProcessLogitsFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, rules):
         # tensors are kept by the graph, not by the context, so that a change in place between
-        # the passes is noticed
+        # the passes is noticed; the logits are read again for the repetition penalty only
         ctx.names = [k for k, v in rules.items() if v is not None]
-        ctx.save_for_backward(logits, *(rules[k] for k in ctx.names))
+        ctx.keeps_logits = rules["repetition"] is not None
+        ctx.save_for_backward(*([logits] if ctx.keeps_logits else []), *(rules[k] for k in ctx.names))
+        ctx.dtype = logits.dtype
         return rp.process_logits_fwd(logits, **rules)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        logits, *kept = ctx.saved_tensors
+        kept = list(ctx.saved_tensors)
         # autograd may hand over an expanded gradient, or one with another column stride
-        if dout.dtype != logits.dtype or dout.stride(-1) != 1 or dout.shape[-1] > 1 and 0 in dout.stride():
-            dout = dout.to(logits.dtype).contiguous()
+        if dout.dtype != ctx.dtype or dout.stride(-1) != 1:
+            dout = dout.to(ctx.dtype).contiguous()
+        logits = kept.pop(0) if ctx.keeps_logits else dout
         return rp.process_logits_bwd(logits, dout, **dict(zip(ctx.names, kept))), None
 
 

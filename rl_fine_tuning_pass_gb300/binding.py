@@ -613,7 +613,7 @@ def topk_log_softmax(logits, K, *, T=1.0):
     ids = torch.empty((R, n), dtype=torch.int64, device=dev)
     logp = torch.empty((R, n), dtype=torch.float32, device=dev)
     lse = torch.empty(R, dtype=torch.float32, device=dev)
-    _call("topk_log_softmax", dev, x, K, T, ids.data_ptr(), logp.data_ptr(), lse.data_ptr())
+    _call("topk_log_softmax", dev, x, K, float(T), ids.data_ptr(), logp.data_ptr(), lse.data_ptr())
     return ids, logp, lse
 
 
@@ -636,7 +636,8 @@ def distill_topk_fwd(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, 
     pi, pt, K = _list_of(ids, teacher_logp, R, dev)
     loss = torch.empty(R, dtype=torch.float32, device=dev)
     lse, p_rest = torch.empty_like(loss), torch.empty_like(loss)
-    _call("distill_topk_fwd", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev), T, beta, bool(tail),
+    _call("distill_topk_fwd", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev), float(T), float(beta),
+          bool(tail),
           loss.data_ptr(), lse.data_ptr(), p_rest.data_ptr(), _on(dev_err, torch.int32, 1, "dev_err", dev))
     return {"loss": loss, "lse": lse, "p_rest": p_rest}
 
@@ -651,8 +652,8 @@ def distill_topk_bwd(logits, ids, teacher_logp, dloss, lse, p_rest, *, T=1.0, be
     pi, pt, K = _list_of(ids, teacher_logp, R, dev)
     f32 = torch.float32
     _call("distill_topk_bwd", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
-          _on(dloss, f32, R, "dloss", dev), _on(lse, f32, R, "lse", dev), _on(p_rest, f32, R, "p_rest", dev), T, beta,
-          bool(tail), dx)
+          _on(dloss, f32, R, "dloss", dev), _on(lse, f32, R, "lse", dev), _on(p_rest, f32, R, "p_rest", dev),
+          float(T), float(beta), bool(tail), dx)
     return dlogits
 
 
@@ -667,6 +668,6 @@ def distill_topk_fused(logits, ids, teacher_logp, dloss, *, T=1.0, beta=0.0, tai
     loss = torch.empty(R, dtype=torch.float32, device=dev)
     lse, p_rest = torch.empty_like(loss), torch.empty_like(loss)
     _call("distill_topk_fused", dev, x, pi, pt, K, _on(mask, torch.uint8, R, "mask", dev),
-          _on(dloss, torch.float32, R, "dloss", dev), T, beta, bool(tail), loss.data_ptr(), lse.data_ptr(),
+          _on(dloss, torch.float32, R, "dloss", dev), float(T), float(beta), bool(tail), loss.data_ptr(), lse.data_ptr(),
           p_rest.data_ptr(), dx, _on(dev_err, torch.int32, 1, "dev_err", dev))
     return {"loss": loss, "lse": lse, "p_rest": p_rest, "dlogits": dlogits}

@@ -102,14 +102,14 @@ struct Scaled {
 __device__ __forceinline__ Scaled over_T(float d, const DistillParams& p) {
   Scaled z;
   z.hi = d * p.invT;
-  z.lo = fmaf(d, p.invT, -z.hi) + d * p.invT_lo;
+  z.lo = fabsf(z.hi) < 1e30f ? fmaf(d, p.invT, -z.hi) + d * p.invT_lo : 0.f;  // (-inf has no rounding)
   return z;
 }
 // e^(d / T), d <= 0 or small
 __device__ __forceinline__ float exp_over_T(float d, const DistillParams& p) {
   const Scaled z = over_T(d, p);
   const float e = expf(z.hi);
-  return fabsf(z.hi) < 1e30f ? fmaf(e, z.lo, e) : e;
+  return fmaf(e, z.lo, e);
 }
 
 // What the teacher's list says (one warp): log q_k = lq_k - shift, the mass of the list and
@@ -154,6 +154,17 @@ __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) 
 __device__ __forceinline__ float rest_ratio(float q, float p, float d) {
   const float e = d / p;
   return fabsf(e) < 0.5f ? log1pf(e) : logf(q / p);
+}
+
+// The unlisted columns' gradient g F p_j as f 2^((x_j - x0) c), from p_j = 2^((x_j - x0) c) scale.
+// Where the student leaves the rest next to nothing, F is of the order of 1 / p_rest: the power of two
+// in p_rest moves from f into x0, so that neither f nor the exponentials leave fp32's range.
+struct Stream {
+  float f, x0;
+};
+__device__ __forceinline__ Stream stream_of(float g, float F, float scale, float x0, float p_rest, float T) {
+  const float lift = p_rest > 0.f && p_rest < 0x1p-30f ? floorf(-log2f(p_rest)) : 0.f;
+  return Stream{g * (F * exp2f(-lift) * scale), x0 - lift * kLn2 * T};
 }
 
 // One row's results (every lane of the list warp); the slots then hold G_k and p_k.
@@ -468,8 +479,9 @@ __global__ void __launch_bounds__(THREADS + 32) distill_kernel(const DistillPara
     if (FUSED) {
       for (int k = lane; k < K; k += 32) sl.lq[k] = bad ? nan : g * (sl.lq[k] - sl.x[k] * o.S);
       if (lane == 0) {
-        sh_factor = g == 0.f ? 0.f : (bad ? nan : g * (o.F_rest - o.S) * o.inv_s);
-        sh_m = o.m;
+        const Stream t = stream_of(g, o.F_rest - o.S, o.inv_s, o.m, o.p_rest, p.T);
+        sh_factor = g == 0.f ? 0.f : (bad ? nan : t.f);
+        sh_m = t.x0;
         sh_stat[0].s = g;
       }
     }
@@ -540,8 +552,10 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
     if (lane == 0) {
       const float x0 = lse * p.T;
       const Scaled z = over_T(x0, p);
-      sh_factor = g * ((p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum) * expf((z.hi - lse) + z.lo);
-      sh_x0 = x0;
+      const Stream st = stream_of(g, (p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum, expf((z.hi - lse) + z.lo), x0, p_rest,
+                                  p.T);
+      sh_factor = st.f;
+      sh_x0 = st.x0;
     }
   }
   __syncthreads();

@@ -491,9 +491,11 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
     }
     if (part.i1 > part.i0) {
       const int k = rr % kStages;
-      const bool came = mbar_wait(smem_addr(&full_bar[k]), phases >> k & 1u);
+      if (!mbar_wait(smem_addr(&full_bar[k]), phases >> k & 1u)) {  // the row is not valid; wait once more for its copy
+        if (tid == 0 && p.dev_err != nullptr) atomicOr(p.dev_err, GRPO_DEVERR_TIMEOUT_BIT);
+        mbar_wait(smem_addr(&full_bar[k]), phases >> k & 1u);
+      }
       phases ^= 1u << k;
-      if (!came && tid == 0 && p.dev_err != nullptr) atomicOr(p.dev_err, GRPO_DEVERR_TIMEOUT_BIT);
       S* buf = reinterpret_cast<S*>(stage(rr));
       auto put = [&](const Hit& a) {
         if (a.at >= 0) E::store_scalar(buf + a.at, h.value(a.col, E::load_shared(buf + a.at), a.x));
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
       }
     }
   }
-  if (tid == 0) bulk_wait_read<0>();
+  if (tid == 0) bulk_wait_all();
 }
 
 // Rows per CTA: long runs count the history seldom, but leave two CTAs or more for each place, and

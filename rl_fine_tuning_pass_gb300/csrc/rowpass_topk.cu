@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   uint32_t* chunks = reinterpret_cast<uint32_t*>(list);
   for (unsigned q = tid; q < min(n, static_cast<unsigned>(cap)); q += T) {
     const uint64_t e = cand[q];
-    if (static_cast<uint32_t>(e >> 32) < least) continue;
+    if (static_cast<uint32_t>(e >> 32) < least || static_cast<uint32_t>(e >> 32) <= key_of(-INFINITY)) continue;
     const unsigned at = atomicAdd(&sh_c, 1u);
     if (at < kChunks) chunks[at] = static_cast<uint32_t>(e);
   }

@@ -126,9 +126,9 @@ def test_confident_students(beta, tail):
     """The list holds all but a sliver of the student's mass, or nearly none of it."""
     V, K = 4000, 16
     x = randn(1, 6, V, seed=5)
-    for r, up in enumerate((8.0, 16.0, 30.0, 60.0)):
+    for r, up in enumerate((8.0, 16.0, 30.0, 60.0, 83.0)):
         x[0, r, 100:100 + K] += up
-    x[0, 4, 3000] += 30.0
+    x[0, 5, 3000] += 30.0
     ids = torch.arange(100, 100 + K).repeat(6, 1)
     lp = torch.log_softmax(randn(6, K + 1, seed=6) * 2, 1)[:, :K].contiguous()
     check(x.to(DEV), ids, lp, 1.0, beta, tail, what="confident")
@@ -205,6 +205,22 @@ def test_infinities_and_nan(beta, tail):
         x[0, 0, int(ids[0, 0])] = float("-inf")
         out = rp.distill_topk_fused(d(x), d(ids), d(lp), w, beta=beta, tail=tail)
         assert float(out["loss"][0]) == float("inf") and bool(out["dlogits"][0, 0].isfinite().all())
+
+
+@pytest.mark.parametrize("beta,tail", WAYS)
+def test_listed_columns_without_mass(beta, tail):
+    """Listed columns whose student logit is -inf: no part of the loss but the teacher's, no NaN in
+    the row; forward, backward and fused."""
+    x = randn(1, 3, 500, seed=2)
+    ids, lp = teacher(x, 7, 1, unused=False)
+    lp[:, 3] = float("-inf")                 # the teacher gives it none either
+    x[0, 0, int(ids[0, 3])] = float("-inf")
+    x[0, 1, int(ids[1, 3])] = -1e30
+    check(x.to(DEV), ids, lp, 0.7, beta, tail, what="no mass")
+    if beta < 1.0 and beta > 0.0:            # the mixture is finite where only the student has none
+        lp[:, 3] = -2.0 - torch.arange(3.0)
+        x[0, 2, int(ids[2, 3])] = float("-inf")
+        check(x.to(DEV), ids, lp, 0.7, beta, tail, what="teacher's mass only")
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

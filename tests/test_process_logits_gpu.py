@@ -284,6 +284,14 @@ def test_autograd_and_other_streams():
     want = lo.process_logits_bwd(f64(x), np.ones((B * L, V)), L, tokens=k["tokens"], hist_len=k["hist_len"],
                                  repetition=k["repetition"])
     close(x.grad, want, 2.0 ** -23 * np.abs(want), "grad of the sum")
+    x.grad = None                                            # without a repetition penalty the logits are not kept
+    few = {n: v for n, v in on_gpu(k).items() if n != "repetition"}
+    h = x * 1.0
+    y = rl.process_logits(h, **few)
+    with torch.no_grad():
+        h.zero_()
+    y.sum().backward()
+    assert bool((x.grad == 1.0).all())
     with pytest.raises(RuntimeError):                        # no second derivative is offered
         g, = torch.autograd.grad(rl.process_logits(x, **d).sum(), x, create_graph=True)
         g.sum().backward()

@@ -122,6 +122,24 @@ def test_rows_without_log_probs():
         check(x[:, [3, 5]].to(dtype).to(DEV), 9)
 
 
+@pytest.mark.parametrize("R", [1, 20, 70, 150, 400])
+def test_masked_rows_at_every_split(R):
+    """Rows left with a few columns (and fewer than K), at the row counts of each number of CTAs."""
+    V, K = 33003, 30
+    g = torch.Generator().manual_seed(R)
+    x = torch.randn(1, R, V, generator=g)
+    x[0, ::3] = torch.where(torch.rand(x[0, ::3].shape, generator=g) < 12 / V, x[0, ::3], -torch.inf)
+    x[0, ::3, V - 1] = 1.0
+    rows = np.unique(np.r_[0, np.arange(0, R, 37), R - 1])
+    for dtype in (torch.bfloat16, torch.float32):
+        xd = x.to(dtype).to(DEV)
+        ids, logp, _ = rp.topk_log_softmax(xd, K)
+        o_ids, o_logp, _ = lo.topk_log_softmax(f64(xd[0, torch.from_numpy(rows).to(DEV)]), K, 1.0)
+        assert np.array_equal(ids.cpu().numpy()[rows], o_ids)
+        close(logp[torch.from_numpy(rows).to(DEV)], o_logp, 1e-5 + 1e-5 * np.abs(np.nan_to_num(o_logp, neginf=0)),
+              "logp")
+
+
 @pytest.mark.parametrize("T", [0.05, 1.0, 50.0])
 def test_temperatures(T):
     x, _ = place(randn(1, 5, 7001, seed=2) * 4, "dense")
