@@ -51,9 +51,6 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void st_cluster_u64(uint32_t cluster_addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr), "l"(v) : "memory");
-}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -178,9 +175,6 @@ struct BF16 {
   __device__ __forceinline__ static float load_scalar_coherent(const storage* p) {
     return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const volatile unsigned short*>(p)) << 16);
   }
-  __device__ __forceinline__ static float load_shared(const storage* p) {
-    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
-  }
   __device__ __forceinline__ static void unpack(const uint4& v, float (&f)[kVec]) {
     f[0] = lo(v.x); f[1] = hi(v.x); f[2] = lo(v.y); f[3] = hi(v.y);
     f[4] = lo(v.z); f[5] = hi(v.z); f[6] = lo(v.w); f[7] = hi(v.w);
@@ -250,7 +244,6 @@ struct F32 {
   __device__ __forceinline__ static float load_scalar_coherent(const storage* p) {
     return *reinterpret_cast<const volatile float*>(p);
   }
-  __device__ __forceinline__ static float load_shared(const storage* p) { return *p; }
   __device__ __forceinline__ static void unpack(const uint4& v, float (&f)[kVec]) {
     f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);

@@ -69,6 +69,13 @@ __device__ __forceinline__ void forbid(uint4& v, uint32_t ok, uint32_t fill, F32
   for (int k = 0; k < 4; ++k) w[k] = ok >> k & 1u ? w[k] : fill;
 }
 
+// An element in shared memory.
+template <class E>
+__device__ __forceinline__ float load_shared(const typename E::storage* p) {
+  if constexpr (sizeof(typename E::storage) == 2) return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+  else return *p;
+}
+
 // Bits j, j + 1, ... of a bitmap of `words` words (at least 25 of them, zeros past its end).
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* m, int j, int words) {
   const int w = j >> 5;
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
       phases ^= 1u << k;
       S* buf = reinterpret_cast<S*>(stage(rr));
       auto put = [&](const Hit& a) {
-        if (a.at >= 0) E::store_scalar(buf + a.at, h.value(a.col, E::load_shared(buf + a.at), a.x));
+        if (a.at >= 0) E::store_scalar(buf + a.at, h.value(a.col, load_shared<E>(buf + a.at), a.x));
       };
       put(mine);
       for (int t = tid + kRulesThreads; t < todo; t += kRulesThreads) put(look(t));

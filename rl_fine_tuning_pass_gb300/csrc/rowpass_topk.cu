@@ -183,6 +183,10 @@ __device__ __forceinline__ uint32_t kth_maximum(const uint16_t* sh, int K) {
   return best;
 }
 
+__device__ __forceinline__ void st_cluster_u64(uint32_t cluster_addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr), "l"(v) : "memory");
+}
+
 struct TopkPart {  // what one CTA of a cluster hands to the first
   float m, s;
   int n;           // entries in its list, -1: its buffers overflowed
