@@ -15,9 +15,10 @@
 // and the touched columns, listed once their run's history is counted, are changed by a thread each:
 // within the stream nearly every warp met one, and its 32 lanes waited for it (1.24 ms against
 // 1.07 ms for forward and backward at (4, 1024, 151936) bf16).
-//   rules_bulk_kernel  no mask, input and output in phase: bulk copies (TMA) into a ring of shared
-//                      memory and out of it; the touched columns are changed there in between.
-//   rules_kernel       any call: the copy goes through registers, with -inf or 0 where the mask
+//   rules_bulk_kernel  input and output in phase: bulk copies (TMA) into a ring of shared memory and
+//                      out of it; mask and touched columns are seen to there in between.
+//   rules_kernel       in place, out of phase, and where launch_e says so: the copy goes through
+//                      registers, with -inf or 0 where the mask
 //                      forbids (vectors that it forbids whole are not read), and the touched
 //                      columns are written over it.
 // Values are formed in fp32 from the whole count and rounded once.
@@ -33,7 +34,7 @@ constexpr int kRulesThreads = 256;
 constexpr int kTileVecs = 1024;  // vectors of a row per CTA, 4 per thread
 constexpr int kPer = kTileVecs / kRulesThreads;
 constexpr int kMaxRun = 8;       // rows per CTA
-constexpr int kBulkRun = 4;      // rows per CTA from which the forward takes the bulk kernel
+constexpr int kBulkRun = 4;      // rows per CTA from which the forward takes the bulk kernel's ring
 constexpr int kWindow = 256;     // tokens past the first row's history that are held ready
 constexpr int kListed = 2048;    // touched columns that are listed; with more, the words are searched
 
@@ -307,6 +308,25 @@ __device__ __forceinline__ int edge_of(const Part& t, int V, int c0, int W) {
   return edge >= c0 && edge < c0 + W ? edge : -1;
 }
 
+// 0 or -inf, in the format of forbid
+template <class E, bool BWD>
+constexpr uint32_t kForbiddenOf = BWD ? 0u : (sizeof(typename E::storage) == 2 ? 0xFF80FF80u : 0xFF800000u);
+
+// Which columns of this thread's vectors i0 + tid + k kRulesThreads < i1 are allowed, a byte each.
+template <class E>
+__device__ __forceinline__ uint32_t allowed_of(const uint32_t* m, int head, int i0, int i1, int mwords) {
+  constexpr uint32_t kAll = (1u << E::kVec) - 1u;
+  uint32_t allowed = 0xFFFFFFFFu;
+  if (m != nullptr) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = i0 + static_cast<int>(threadIdx.x) + k * kRulesThreads;
+      if (i < i1) allowed ^= (bits_at(m, head + i * E::kVec, mwords) & kAll ^ kAll) << (8 * k);
+    }
+  }
+  return allowed;
+}
+
 // Grid: tiles x runs, tiles innermost.  run: rows per CTA, runs: runs per sequence.
 // HOW: the input and output rows.
 enum RulesHow : int {
@@ -333,7 +353,7 @@ __global__ void __launch_bounds__(kRulesThreads, BWD ? 4 : 3) rules_kernel(const
   H h(p, sh, reinterpret_cast<uint32_t*>(rules_smem), b, l0, nrows, c0);
 
   constexpr uint32_t kAll = (1u << VEC) - 1u;
-  constexpr uint32_t kForbidden = BWD ? 0u : (sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u);  // 0 or -inf
+  constexpr uint32_t kForbidden = kForbiddenOf<E, BWD>;
   for (int rr = 0; rr < nrows; ++rr) {
     const int64_t l = l0 + rr;
     S* out = static_cast<S*>(p.out.ptr) + b * p.out.sb + l * p.out.sl;
@@ -348,14 +368,7 @@ __global__ void __launch_bounds__(kRulesThreads, BWD ? 4 : 3) rules_kernel(const
     uint4 v[kPer];
     if constexpr (HOW == kOutOfPhase)
       load_out_of_phase<E, kPer, kRulesThreads>(v, src + sp.head, i0 + tid, i1, sp.nvec);
-    uint32_t allowed = 0xFFFFFFFFu;
-    if (m != nullptr) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int i = i0 + tid + k * kRulesThreads;
-        if (i < i1) allowed ^= (bits_at(m, sp.head + i * VEC, mwords) & kAll ^ kAll) << (8 * k);
-      }
-    }
+    const uint32_t allowed = allowed_of<E>(m, sp.head, i0, i1, mwords);
     auto full = [&](int k) { return (allowed >> (8 * k) & kAll) == kAll; };
     auto none = [&](int k) { return (allowed >> (8 * k) & kAll) == 0u; };
     if constexpr (HOW != kOutOfPhase) {
@@ -427,14 +440,15 @@ __global__ void __launch_bounds__(kRulesThreads, BWD ? 4 : 3) rules_kernel(const
 template <bool BWD>
 constexpr int kStagesOf = BWD ? 2 : 4;
 
-template <class E, bool BWD>
+// MASK: there is one.  STAGES: of the ring (1: runs of one row).
+template <class E, bool BWD, bool MASK, int STAGES>
 __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesParams p, int tiles, int run, int runs) {
   using H = History<E, BWD>;
   using S = typename E::storage;
-  constexpr int VEC = E::kVec, W = H::W, kStages = kStagesOf<BWD>;
+  constexpr int VEC = E::kVec, W = H::W;
   extern __shared__ uint4 rules_smem[];  // the ring, then the words
   __shared__ typename H::Shared sh;
-  __shared__ __align__(8) uint64_t full_bar[kStages];
+  __shared__ __align__(8) uint64_t full_bar[STAGES];
   wait_for_previous_grids();
   const int tid = threadIdx.x;
   const int c0 = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles)) * W;
@@ -442,27 +456,27 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
   const int64_t b = seq_run / static_cast<unsigned>(runs);
   const int64_t l0 = static_cast<int64_t>(seq_run % static_cast<unsigned>(runs)) * run;
   const int nrows = static_cast<int>(min(static_cast<int64_t>(run), p.x.L - l0));
-  const int V = p.x.V;
+  const int V = p.x.V, mwords = (V + 31) >> 5;
   auto out_row = [&](int rr) { return static_cast<S*>(p.out.ptr) + b * p.out.sb + (l0 + rr) * p.out.sl; };
   auto src_row = [&](int rr) {
     return BWD ? static_cast<const S*>(p.dy.ptr) + b * p.dy.sb + (l0 + rr) * p.dy.sl
                : static_cast<const S*>(p.x.ptr) + b * p.x.sb + (l0 + rr) * p.x.sl;
   };
-  auto stage = [&](int rr) { return rules_smem + (rr % kStages) * kTileVecs; };
+  auto stage = [&](int rr) { return rules_smem + (rr % STAGES) * kTileVecs; };
   auto fill = [&](int rr) {  // thread 0: start the copy of row rr's part into its stage
     const Part t = part_of<E>(out_row(rr), V, c0);
     if (t.i1 <= t.i0) return;
-    const uint32_t bar = smem_addr(&full_bar[rr % kStages]);
+    const uint32_t bar = smem_addr(&full_bar[rr % STAGES]);
     const uint32_t bytes = static_cast<uint32_t>(t.i1 - t.i0) * 16u;
     mbar_expect(bar, bytes);
     bulk_load(smem_addr(stage(rr)), src_row(rr) + t.sp.head + static_cast<int64_t>(t.i0) * VEC, bytes, bar);
   };
   if (tid == 0) {
-    for (int k = 0; k < kStages; ++k) mbar_init(smem_addr(&full_bar[k]), 1u);
+    for (int k = 0; k < STAGES; ++k) mbar_init(smem_addr(&full_bar[k]), 1u);
     mbar_init_fence();
-    for (int k = 0; k < kStages && k < nrows; ++k) fill(k);
+    for (int k = 0; k < STAGES && k < nrows; ++k) fill(k);
   }
-  H h(p, sh, reinterpret_cast<uint32_t*>(rules_smem + kStages * kTileVecs), b, l0, nrows, c0);
+  H h(p, sh, reinterpret_cast<uint32_t*>(rules_smem + STAGES * kTileVecs), b, l0, nrows, c0);
   __syncthreads();  // the barriers are there
 
   uint32_t phases = 0u;  // bit k: the parity that stage k's next copy completes
@@ -471,6 +485,8 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
     const S* src = src_row(rr);
     const Part part = part_of<E>(out, V, c0);
     const RowSplit sp = part.sp;
+    const uint32_t* m = MASK ? p.allowed + b * p.allowed_sb + (l0 + rr) * p.allowed_sl : nullptr;
+    const uint32_t allowed = allowed_of<E>(m, sp.head, part.i0, part.i1, mwords);
     h.go_to(rr);
     const int todo = h.todo();
     const S* x = BWD ? static_cast<const S*>(p.x.ptr) + b * p.x.sb + (l0 + rr) * p.x.sl : nullptr;
@@ -483,6 +499,7 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
       Hit a{h.col_at(t), -1, 0.f};
       const int at = c0 + a.col - sp.head - part.i0 * VEC;
       if (a.col < 0 || at < 0 || at >= (part.i1 - part.i0) * VEC) return a;
+      if (MASK && (bits_at(m, c0 + a.col, mwords) & 1u) == 0) return a;
       a.at = at;
       if (BWD) a.x = E::load_scalar_coherent(x + c0 + a.col);
       return a;
@@ -493,16 +510,30 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
     const int edge = edge_of(part, V, c0, W);
     if (edge >= 0) {
       float f = E::load_scalar_coherent(src + edge);
-      if (todo > 0 && h.is_touched(edge - c0)) f = h.value(edge - c0, f, BWD ? E::load_scalar_coherent(x + edge) : 0.f);
+      if (MASK && (bits_at(m, edge, mwords) & 1u) == 0) f = BWD ? 0.f : -INFINITY;
+      else if (todo > 0 && h.is_touched(edge - c0)) f = h.value(edge - c0, f, BWD ? E::load_scalar_coherent(x + edge) : 0.f);
       E::store_scalar(out + edge, f);
     }
     if (part.i1 > part.i0) {
-      const int k = rr % kStages;
+      const int k = rr % STAGES;
       if (!mbar_wait(smem_addr(&full_bar[k]), phases >> k & 1u)) {  // the row is not valid; wait once more for its copy
         if (tid == 0 && p.dev_err != nullptr) atomicOr(p.dev_err, GRPO_DEVERR_TIMEOUT_BIT);
         mbar_wait(smem_addr(&full_bar[k]), phases >> k & 1u);
       }
       phases ^= 1u << k;
+      if (MASK) {  // -inf or 0 where the mask forbids; touched columns that it forbids are left
+        uint4* vb = stage(rr);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const int i = tid + q * kRulesThreads;
+          const uint32_t ok = allowed >> (8 * q) & ((1u << VEC) - 1u);
+          if (part.i0 + i >= part.i1 || ok == (1u << VEC) - 1u) continue;
+          uint4 v = vb[i];
+          forbid(v, ok, kForbiddenOf<E, BWD>, static_cast<E*>(nullptr));
+          vb[i] = v;
+        }
+        __syncthreads();
+      }
       S* buf = reinterpret_cast<S*>(stage(rr));
       auto put = [&](const Hit& a) {
         if (a.at >= 0) E::store_scalar(buf + a.at, h.value(a.col, load_shared<E>(buf + a.at), a.x));
@@ -518,9 +549,9 @@ __global__ void __launch_bounds__(kRulesThreads) rules_bulk_kernel(const RulesPa
                    static_cast<uint32_t>(part.i1 - part.i0) * 16u);
       bulk_commit();
       // the row before has left its stage: the next copy into it
-      if (rr >= 1 && rr - 1 + kStages < nrows) {
+      if (rr >= 1 && rr - 1 + STAGES < nrows) {
         bulk_wait_read<1>();
-        fill(rr - 1 + kStages);
+        fill(rr - 1 + STAGES);
       }
     }
   }
@@ -536,6 +567,19 @@ int64_t pick_run(int64_t rows, int64_t L, int tiles, int64_t places) {
   return run < L ? run : L;
 }
 
+template <class E, bool BWD, bool MASK, int STAGES>
+cudaError_t launch_bulk(const RulesParams& p, dim3 grid, int tiles, int64_t run, int64_t runs, int words,
+                        cudaStream_t s) {
+  constexpr int ring = STAGES * kTileVecs * 16, most = ring + History<E, BWD>::WORDS * 4;
+  if (most > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(rules_bulk_kernel<E, BWD, MASK, STAGES>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_after_previous_smem(rules_bulk_kernel<E, BWD, MASK, STAGES>, grid, dim3(kRulesThreads), ring + words, s,
+                                    p, tiles, static_cast<int>(run), static_cast<int>(runs));
+}
+
 template <class E, bool BWD, int HOW>
 cudaError_t launch_e(const RulesParams& p, int64_t rows, int sms, cudaStream_t s) {
   using H = History<E, BWD>;
@@ -546,14 +590,17 @@ cudaError_t launch_e(const RulesParams& p, int64_t rows, int sms, cudaStream_t s
   const int64_t run = pick_run(rows, p.x.L, tiles, 4LL * sms), runs = (p.x.L + run - 1) / run;
   const dim3 grid(static_cast<unsigned>(rows / p.x.L * runs * tiles)), block(kRulesThreads);
   if constexpr (HOW == kInPhase) {
-    if (p.allowed == nullptr && (BWD || run >= kBulkRun)) {
-      constexpr int ring = kStagesOf<BWD> * kTileVecs * 16, most = ring + H::WORDS * 4;
-      const cudaError_t e =
-          cudaFuncSetAttribute(rules_bulk_kernel<E, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-      if (e != cudaSuccess) return e;
-      return launch_after_previous_smem(rules_bulk_kernel<E, BWD>, grid, block, ring + words, s, p, tiles,
-                                        static_cast<int>(run), static_cast<int>(runs));
-    }
+    // One row: its part is all that the ring holds, and more CTAs share an SM (64 decode rows of 151936
+    // under masks: 20 us, 24 us through registers).  The forward's longer ring pays from runs of four
+    // rows (runs of two, 510 rows of 32003 fp32: 29 us, 24 us through registers), and not with a mask,
+    // which lets the registers leave out what it forbids (there 43 us, against 31 us).
+    constexpr int many = kStagesOf<BWD>;
+    if (run == 1)
+      return p.allowed ? launch_bulk<E, BWD, true, 1>(p, grid, tiles, run, runs, words, s)
+                       : launch_bulk<E, BWD, false, 1>(p, grid, tiles, run, runs, words, s);
+    if (p.allowed == nullptr && (BWD || run >= kBulkRun))
+      return launch_bulk<E, BWD, false, many>(p, grid, tiles, run, runs, words, s);
+    if constexpr (BWD) return launch_bulk<E, BWD, true, many>(p, grid, tiles, run, runs, words, s);
   }
   return launch_after_previous_smem(rules_kernel<E, BWD, HOW>, grid, block, words, s, p, tiles, static_cast<int>(run),
                                     static_cast<int>(runs));
