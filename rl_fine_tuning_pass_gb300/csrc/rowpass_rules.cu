@@ -9,18 +9,20 @@
 // A CTA takes one tile of columns (1024 vectors) of a run of rows of one sequence.  The history of
 // the run's first row is counted into one 32-bit word per column in shared memory (logits_ops.h);
 // from row to row only the tokens that have come in are added (a row whose history is shorter
-// than the one before starts anew), so the history is read once per run and tile, not once per row.  The gradient needs only which columns occur, and keeps no words but bits.
+// than the one before starts anew), so the history is read once per run and tile, not once per
+// row (without runs: 2.29 ms for forward and backward at (4, 1024, 151936) bf16, with them 1.66 ms).
+// The gradient needs only which columns occur, and keeps no words but bits.
 //
 // The pass is bound by HBM (read and write every logit once), so the stream over a row is a copy,
 // and the touched columns, listed once their run's history is counted, are changed by a thread each:
-// within the stream nearly every warp met one, and its 32 lanes waited for it (1.24 ms against
-// 1.07 ms for forward and backward at (4, 1024, 151936) bf16).
+// within the stream nearly every warp met one, and its 32 lanes waited for it (1.24 ms; 1.07 ms with
+// the list).
 //   rules_bulk_kernel  input and output in phase: bulk copies (TMA) into a ring of shared memory and
-//                      out of it; mask and touched columns are seen to there in between.
+//                      out of it; mask and touched columns are seen to there in between (0.79 ms,
+//                      6.3 TB/s of the two passes' 4.98 GB).
 //   rules_kernel       in place, out of phase, and where launch_e says so: the copy goes through
-//                      registers, with -inf or 0 where the mask
-//                      forbids (vectors that it forbids whole are not read), and the touched
-//                      columns are written over it.
+//                      registers, with -inf or 0 where the mask forbids (vectors that it forbids whole
+//                      are not read), and the touched columns are written over it.
 // Values are formed in fp32 from the whole count and rounded once.
 #include "logits_load.cuh"
 #include "logits_ops.h"

@@ -1,18 +1,22 @@
 // The K largest log-probs of each row, log_softmax(x / T), with their columns: sorted, ties
 // to the lowest column.
 //
-// One sweep over the row forms the softmax statistic (logits_stat.cuh) and notes where
-// candidates are.  Each thread keeps the largest element it has met in the even and in the odd
-// places of its vectors, 512 maxima per CTA (up to K = 64 one of both, 256); the K-th largest of those maxima is a lower bound of
-// the K-th largest element seen so far (K different elements reach it), so a chunk (the vectors of
-// one thread in one step) without an element that reaches it cannot hold a result.  The bound is
-// taken anew after 1, 4, 16, ... steps of the sweep and at its end: of N(0, 1) elements about 64
-// chunks of the first step reach it at K = 64, and three times as many of each quadrupling, some 460
-// of a row of 151936 (a bound after each doubling notes fewer chunks and waits at more barriers:
-// 2048 rows of 32000 at K = 128 took 62 us, against 59 us).  The
-// chunks that also reach the last bound (about 64) are read again, and their elements that reach
-// it (about 70) are ranked by counting.  With few rows, where a CTA's
-// part is a few steps, all its chunks are noted and the bound is taken once, at the end.
+// One sweep over the row forms the softmax statistic (logits_stat.cuh) and notes where candidates
+// are.  Each thread keeps the largest element it has met in the even and in the odd places of its
+// vectors, 512 maxima per CTA (up to K = 64 one of both, 256); the K-th largest of those maxima is a
+// lower bound of the K-th largest element seen so far (K different elements reach it), so a chunk
+// (the vectors of one thread in one step) without an element that reaches it cannot hold a result.
+// The bound is taken anew after 1, 4, 16, ... steps of the sweep and at its end: of N(0, 1) elements
+// about 64 chunks of the first step reach it at K = 64, and three times as many of each quadrupling,
+// some 460 of a row of 151936 (a bound after each doubling notes fewer chunks and waits at more
+// barriers: 2048 rows of 32000 at K = 128 took 62 us, against 59 us).  The chunks that also reach the
+// last bound (about 64) are listed and read again, and their elements that reach it (about 70) are
+// ranked by counting.  With few rows, where a CTA's part is a few steps, all its chunks are noted and
+// the bound is taken once, at the end.
+//
+// Measured: the top 64 of 8192 rows of 151936 bf16 take 423 us (5.9 TB/s, 87% of the copy rate; radix
+// selection alone took 4.2 ms), of which the DRAM reads are 1.07 times the row; what is left are the
+// barriers of the bounds and of the ranking, which five CTAs per SM do not hide whole.
 //
 // Rows that collect more than the buffers hold (thousands of ties at the K-th value, large
 // values that come last) are done again by radix selection on order-preserving keys.
