@@ -296,16 +296,16 @@ __host__ __device__ inline int bitmap_bytes(int V) {
   return need < kBitmapBytes ? static_cast<int>(need) : kBitmapBytes;
 }
 
-// out_j = f 2^((x_j - x0) c) over the row (the streaming threads).  With kept_vecs > 0, body
-// vectors [0, kept_vecs) come from `kept` in shared memory, after the others.
+// out_j = f 2^((x_j - x0) c) over the span (the streaming threads).  With kept_vecs > 0 (the span is
+// the row) body vectors [0, kept_vecs) come from `kept` in shared memory, after the others.
 template <class E, int THREADS, int UNROLL, bool SAME_PHASE>
 __device__ __forceinline__ void grad_stream(const typename E::storage* in, typename E::storage* out,
-                                            const RowSplit& sp, float x0, float c, float f,
+                                            const RowSplit& sp, const Span& sn, float x0, float c, float f,
                                             const uint4* kept = nullptr, int kept_vecs = 0) {
   const int tid = threadIdx.x;
   auto scalar = [&](int j) { E::store_scalar(out + j, f * ex2((E::load_scalar_coherent(in + j) - x0) * c)); };
-  if (tid < sp.head) scalar(tid);
-  if (tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
+  if (sn.head && tid < sp.head) scalar(tid);
+  if (sn.tail && tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
   const typename E::storage* ib = in + sp.head;
   uint4* ob = reinterpret_cast<uint4*>(out + sp.head);
   const float2 c2 = make_float2(c, c), n0 = make_float2(-x0, -x0), f2 = make_float2(f, f);
@@ -337,17 +337,32 @@ __device__ __forceinline__ void grad_stream(const typename E::storage* in, typen
     }
   };
   if constexpr (SAME_PHASE) {
-    sweep([&](int j) { return ld_v4_evict_first(reinterpret_cast<const uint4*>(ib) + j); }, kept_vecs + tid, sp.nvec);
+    sweep([&](int j) { return ld_v4_evict_first(reinterpret_cast<const uint4*>(ib) + j); }, sn.v0 + kept_vecs + tid,
+          sn.v1);
   } else {
-    for (int i = tid; i < sp.nvec; i += UNROLL * THREADS) {
+    for (int i = sn.v0 + tid; i < sn.v1; i += UNROLL * THREADS) {
       uint4 v[UNROLL];
-      load_out_of_phase<E, UNROLL, THREADS>(v, ib, i, sp.nvec, sp.nvec);
+      load_out_of_phase<E, UNROLL, THREADS>(v, ib, i, sn.v1, sp.nvec);
 #pragma unroll
       for (int k = 0; k < UNROLL; ++k)
-        if (i + k * THREADS < sp.nvec) process(v[k], i + k * THREADS);
+        if (i + k * THREADS < sn.v1) process(v[k], i + k * THREADS);
     }
   }
   if (kept_vecs > 0) sweep([&](int j) { return kept[j]; }, tid, kept_vecs);
+}
+
+// Part `part` of `parts` of a row: an equal share of its vectors, the head with the first, the tail
+// with the last.
+__device__ __forceinline__ Span span_of(const RowSplit& sp, int part, int parts) {
+  const int share = (sp.nvec + parts - 1) / parts;
+  const int v0 = min(sp.nvec, part * share);
+  return Span{v0, min(sp.nvec, v0 + share), part == 0, part == parts - 1};
+}
+template <class E>
+__device__ __forceinline__ bool in_span(const RowSplit& sp, const Span& sn, int j) {
+  if (j < sp.head) return sn.head;
+  const int i = (j - sp.head) / E::kVec;
+  return i >= sp.nvec ? sn.tail : i >= sn.v0 && i < sn.v1;
 }
 
 // Forward, or (FUSED) forward and backward in one kernel: the row is swept again for the gradient
@@ -355,22 +370,26 @@ __device__ __forceinline__ void grad_stream(const typename E::storage* in, typen
 // memory, as in fused_kernel.
 // The forward of many rows is held to the registers that let five CTAs share an SM (8192 rows of 304
 // KB: 279 us, 300 us with four).
-template <class E, int THREADS, int UNROLL, bool FUSED, bool SAME_PHASE>
-__global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0) distill_kernel(const DistillParams p, int bm_bytes, int keep_vecs) {
+// CS > 1 (forward of few rows): a cluster of CTAs takes a row, a part each; the first one gets the
+// parts' statistics and finishes the row.
+template <class E, int THREADS, int UNROLL, bool FUSED, bool SAME_PHASE, int CS>
+__global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0)
+    distill_kernel(const DistillParams p, int bm_bytes, int keep_vecs) {
   using S = typename E::storage;
   constexpr int kWarps = THREADS / 32;
   extern __shared__ uint4 distill_smem[];
-  __shared__ MaxStat sh_stat[kWarps];
+  __shared__ MaxStat sh_stat[kWarps], sh_parts[CS];
   __shared__ float sh_factor, sh_m;
   __shared__ __align__(8) uint64_t kept_bar;
   wait_for_previous_grids();
-  const int64_t r = blockIdx.x;
+  const int rank = CS > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t r = blockIdx.x / CS;
   const int64_t b = r / p.x.L, l = r - b * p.x.L;
   const int tid = threadIdx.x, V = p.x.V, K = p.K;
   const bool list_warp = tid >= THREADS;
   S* out = FUSED ? static_cast<S*>(p.dx.ptr) + b * p.dx.sb + l * p.dx.sl : nullptr;
   if (p.mask != nullptr && p.mask[r] == 0) {
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
       p.loss[r] = 0.f;
       p.lse[r] = 0.f;
       p.p_rest[r] = 0.f;
@@ -381,8 +400,10 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
     }
     return;
   }
+  if (CS > 1) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
   const S* row = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
   const RowSplit sp = split_row<E>(row, V);
+  const Span sn = span_of(sp, rank, CS);
   uint4* kept = distill_smem;
   uint4* bits = kept + (FUSED ? keep_vecs : 0);
   const Slots sl = slots_at(reinterpret_cast<char*>(bits) + bm_bytes, K);
@@ -425,8 +446,8 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
       if (bm.get(j) && (!bm.wraps() || listed_bits(sl, K, j, 1))) return;
       maxrun_scalar(rs, FUSED ? E::load_scalar_coherent(row + j) : E::load_scalar(row + j), c);
     };
-    if (tid < sp.head) scalar(tid);
-    if (tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
+    if (sn.head && tid < sp.head) scalar(tid);
+    if (sn.tail && tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
     auto leave_out = [&](uint4& v, int i) {
       uint32_t w = bm.vec(i);
       if (w != 0u) {
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
       }
     };
     // FUSED: coherent loads (dlogits may alias the logits), kept in L2 for the second sweep
-    sweep([&](int i) { return FUSED ? ld_v4_evict_last(vb + i) : ld_nc_v4(vb + i); }, kv + tid, sp.nvec);
+    sweep([&](int i) { return FUSED ? ld_v4_evict_last(vb + i) : ld_nc_v4(vb + i); }, sn.v0 + kv + tid, sn.v1);
     if (FUSED && kv > 0) {
       if (!kept_copy_wait(bar)) {  // the row's outputs are not valid; wait once more for the copies in flight
         if (tid == 0 && p.dev_err != nullptr) atomicOr(p.dev_err, GRPO_DEVERR_TIMEOUT_BIT);
@@ -470,9 +491,25 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
     if ((tid & 31) == 0) sh_stat[tid >> 5] = st;
   }
   __syncthreads();
+  if (CS > 1) {
+    cluster_wait();
+    if (list_warp) {
+      const int lane = tid - THREADS;
+      const MaxStat st = maxstat_warp(lane < kWarps ? sh_stat[lane] : MaxStat{-FLT_MAX, 0.f}, c);
+      if (lane == 0) {
+        const uint32_t to = map_to_rank(smem_addr(&sh_parts[rank]), 0);
+        st_cluster_f32(to, st.m);
+        st_cluster_f32(to + 4u, st.s);
+      }
+    }
+    cluster_sync();
+    if (rank != 0) return;
+  }
   if (list_warp) {
     const int lane = tid - THREADS;
-    const MaxStat st = maxstat_warp(lane < kWarps ? sh_stat[lane] : MaxStat{-FLT_MAX, 0.f}, c);
+    constexpr int kStats = CS > 1 ? CS : kWarps;
+    const MaxStat* stats = CS > 1 ? sh_parts : sh_stat;
+    const MaxStat st = maxstat_warp(lane < kStats ? stats[lane] : MaxStat{-FLT_MAX, 0.f}, c);
     const float g = FUSED ? p.dloss[r] / p.T : 0.f;
     const RowResult o = finish_row(sl, K, te, st, p);
     const float nan = __int_as_float(0x7FC00000);
@@ -501,7 +538,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
       fill_span<E, THREADS>(out, osp, whole_row(osp), 0u);
       l2_demote<THREADS>(row, static_cast<int64_t>(V) * sizeof(S));  // not read again after all
     } else {
-      grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, osp, sh_m, c, f, kept, kv);
+      grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, osp, whole_row(osp), sh_m, c, f, kept, kv);
     }
   }
   if (g == 0.f) return;  // +0.0 everywhere
@@ -514,12 +551,13 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
 // The backward: the list warp works out the row's factor and the listed columns' gradients, then
 // the others stream the row as rowgrad_kernel does.
 template <class E, int THREADS, int UNROLL, bool SAME_PHASE>
-__global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const DistillParams p, int parts) {
   using S = typename E::storage;
   extern __shared__ uint4 distill_smem[];
   __shared__ float sh_factor, sh_x0;
   wait_for_previous_grids();
-  const int64_t r = blockIdx.x;
+  const int64_t r = blockIdx.x / static_cast<unsigned>(parts);
+  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
   const int64_t b = r / p.x.L, l = r - b * p.x.L;
   const int tid = threadIdx.x, V = p.x.V, K = p.K;
   const bool list_warp = tid >= THREADS;
@@ -528,15 +566,16 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
   S* out = static_cast<S*>(p.dx.ptr) + b * p.dx.sb + l * p.dx.sl;
   const S* row = static_cast<const S*>(p.x.ptr) + b * p.x.sb + l * p.x.sl;
   const RowSplit sp = split_row<E>(out, V);
+  const Span sn = span_of(sp, part, parts);
   if (g == 0.f) {
-    if (!list_warp) fill_span<E, THREADS>(out, sp, whole_row(sp), 0u);
+    if (!list_warp) fill_span<E, THREADS>(out, sp, sn, 0u);
     return;
   }
   const Slots sl = slots_at(distill_smem, K);
   // long rows: their start comes to L2 while the list is worked on (999 rows of 200 KB: 64 us against
   // 67 us; rows of 64 KB took longer with it)
-  const int64_t row_bytes = static_cast<int64_t>(V) * sizeof(S);
-  if (tid == 0 && row_bytes >= 131072) prefetch_row(row, row_bytes);
+  const int64_t span_bytes = static_cast<int64_t>(sn.v1 - sn.v0) * 16;
+  if (tid == 0 && span_bytes >= 131072) prefetch_row(row + sp.head + static_cast<int64_t>(sn.v0) * E::kVec, span_bytes);
   if (list_warp) {
     const int lane = tid - THREADS;
     const float lse = p.lse[r], p_rest = p.p_rest[r];
@@ -571,58 +610,87 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
   __syncthreads();
   if (!list_warp) {
     const float f = sh_factor;
-    if (f == 0.f) fill_span<E, THREADS>(out, sp, whole_row(sp), 0u);
-    else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, sp, sh_x0, p.c, f);
+    if (f == 0.f) fill_span<E, THREADS>(out, sp, sn, 0u);
+    else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, sp, sn, sh_x0, p.c, f);
   }
   __syncthreads();  // the listed columns' values go over the stream's
   if (list_warp)
     for (int k = tid - THREADS; k < K; k += 32)
-      if (sl.id[k] >= 0) E::store_scalar(out + sl.id[k], sl.lq[k]);
+      if (sl.id[k] >= 0 && in_span<E>(sp, sn, sl.id[k])) E::store_scalar(out + sl.id[k], sl.lq[k]);
 }
 
-template <class E, int THREADS, int U, bool FUSED, bool SAME_PHASE>
+template <class E, int THREADS, int U, bool FUSED, bool SAME_PHASE, int CS = 1>
 cudaError_t launch_distill_k(const DistillParams& p, int64_t rows, int keep_bytes, cudaStream_t s) {
   const int bm = bitmap_bytes<E>(p.x.V);
   const size_t smem = static_cast<size_t>(keep_bytes) + bm + 12 * static_cast<size_t>(p.K);
+  auto* kernel = distill_kernel<E, THREADS, U, FUSED, SAME_PHASE, CS>;
   if (smem > 46 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(distill_kernel<E, THREADS, U, FUSED, SAME_PHASE>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kFusedKeepBytes + kBitmapBytes + 12 * kDistillMaxK);
     if (e != cudaSuccess) return e;
   }
-  return launch_after_previous_smem(distill_kernel<E, THREADS, U, FUSED, SAME_PHASE>,
-                                    dim3(static_cast<unsigned>(rows)), dim3(THREADS + 32), smem, s, p, bm,
-                                    keep_bytes / 16);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * CS));
+  cfg.blockDim = dim3(THREADS + 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, bm, keep_bytes / 16);
+}
+
+// CTAs per row: as many (8 at most) as keep `places` CTAs at once, each with a step of its sweep
+// (1024 vectors) or more.
+template <class E>
+int row_parts(const DistillParams& p, int64_t rows, int64_t places) {
+  int n = 1;
+  while (n < 8 && rows * n * 2 <= places && p.x.V / E::kVec >= 2048 * n) n *= 2;
+  return n;
 }
 
 // Streaming threads of the forward, and vectors in flight of each: 64 x 4 for short rows; 128 x 8 while
 // that leaves most rows resident (7 such CTAs per SM: 2048 rows of 64 KB 26 us, against 30 us with
-// 256 x 4 and 34 us with 256 x 8, whose last step is mostly empty); else 256 x 4.
+// 256 x 4 and 34 us with 256 x 8, whose last step is mostly empty), in clusters while rows leave SMs
+// idle; else 256 x 4.
 template <class E>
 cudaError_t launch_distill_fwd_e(const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
   if (static_cast<int64_t>(p.x.V) * sizeof(typename E::storage) <= 8192)
     return launch_distill_k<E, 64, kUnroll, false, true>(p, rows, 0, s);
+  switch (row_parts<E>(p, rows, 7LL * sms)) {
+    case 8: return launch_distill_k<E, 128, 8, false, true, 8>(p, rows, 0, s);
+    case 4: return launch_distill_k<E, 128, 8, false, true, 4>(p, rows, 0, s);
+    case 2: return launch_distill_k<E, 128, 8, false, true, 2>(p, rows, 0, s);
+    default: break;
+  }
   return rows <= 20LL * sms ? launch_distill_k<E, 128, 8, false, true>(p, rows, 0, s)
                             : launch_distill_k<E, 256, kUnroll, false, true>(p, rows, 0, s);
 }
 
 template <class E, int THREADS, int U>
-cudaError_t launch_distill_bwd_t(bool same_phase, const DistillParams& p, int64_t rows, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(rows)), block(THREADS + 32);
+cudaError_t launch_distill_bwd_t(bool same_phase, const DistillParams& p, int64_t rows, int parts, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(rows * parts)), block(THREADS + 32);
   const size_t smem = 12 * static_cast<size_t>(p.K);
-  return same_phase ? launch_after_previous_smem(distill_bwd_kernel<E, THREADS, U, true>, grid, block, smem, s, p)
-                    : launch_after_previous_smem(distill_bwd_kernel<E, THREADS, kUnroll, false>, grid, block, smem, s,
-                                                 p);
+  return same_phase
+             ? launch_after_previous_smem(distill_bwd_kernel<E, THREADS, U, true>, grid, block, smem, s, p, parts)
+             : launch_after_previous_smem(distill_bwd_kernel<E, THREADS, kUnroll, false>, grid, block, smem, s, p, parts);
 }
 
-// Long rows with eight vectors in flight per thread (8192 rows of 304 KB: 662 us against 673 us).
+// Long rows with eight vectors in flight per thread (8192 rows of 304 KB: 662 us against 673 us); few
+// rows in parts, a CTA each.
 template <class E>
 cudaError_t launch_distill_bwd_e(bool same_phase, const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
   const int64_t bytes = static_cast<int64_t>(p.x.V) * sizeof(typename E::storage);
   if (pick_threads_bwd(p.x.V, sizeof(typename E::storage), rows, sms) == 64)
-    return launch_distill_bwd_t<E, 64, kUnroll>(same_phase, p, rows, s);
-  return bytes < 131072 ? launch_distill_bwd_t<E, 256, kUnroll>(same_phase, p, rows, s)
-                        : launch_distill_bwd_t<E, 256, 8>(same_phase, p, rows, s);
+    return launch_distill_bwd_t<E, 64, kUnroll>(same_phase, p, rows, 1, s);
+  const int parts = row_parts<E>(p, rows, 5LL * sms);
+  return bytes / parts < 131072 ? launch_distill_bwd_t<E, 256, kUnroll>(same_phase, p, rows, parts, s)
+                                : launch_distill_bwd_t<E, 256, 8>(same_phase, p, rows, parts, s);
 }
 
 template <class E, int THREADS, int U>

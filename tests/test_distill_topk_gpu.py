@@ -121,6 +121,39 @@ def test_long_rows(beta, tail):
         check(x.to(DEV), ids, lp, 1.0, beta, tail, what=f"V={V}")
 
 
+@pytest.mark.parametrize("R", [5, 180, 400, 1200])
+@pytest.mark.parametrize("dtype,V,layout", [(torch.bfloat16, 70003, "cut"), (torch.float32, 40001, "odd")])
+def test_row_counts(R, dtype, V, layout):
+    """Batches of every split of rows over CTAs (clusters in the forward, parts in the backward),
+    masked rows among them: some rows against the oracle, every row against the rows alone."""
+    x, _ = place((randn(1, R, V, seed=R) * 2).to(dtype), layout)
+    ids, lp = teacher(x.cpu(), 20, 1)
+    ids[:, 0] = torch.where(ids[:, 1] != 0, 0, ids[:, 0])                # the first column
+    ids[:, 2] = torch.where((ids != V - 1).all(1), V - 1, ids[:, 2])     # and the last one
+    dup = torch.tensor([len(set(r.tolist()) - {-1}) < int((r >= 0).sum()) for r in ids])
+    ids[dup] = torch.arange(20)                                          # no column twice
+    mask = (torch.arange(R) % 7 != 3).to(torch.uint8)
+    w = randn(R, seed=3)
+    d = lambda t: t.to(DEV)  # noqa: E731
+    how = dict(T=0.8, beta=0.5, tail=True)
+    f = rp.distill_topk_fwd(x, d(ids), d(lp), **how, mask=d(mask))
+    dl = rp.distill_topk_bwd(x, d(ids), d(lp), d(w), f["lse"], f["p_rest"], **how, mask=d(mask))
+    fused = rp.distill_topk_fused(x, d(ids), d(lp), d(w), **how, mask=d(mask))
+    rows = np.unique(np.r_[0, 3, R // 2, R - 1, np.arange(0, R, 97)])
+    at = torch.from_numpy(rows)
+    xs, T = f64(x[0, at.to(DEV)]), float(np.float32(0.8))
+    o = lo.distill_topk(xs, ids[at].numpy(), lp[at].numpy(), T, 0.5, True, mask[at].numpy(), w[at].double().numpy())
+    tol = tolerances(o, xs, ids[at].numpy(), w[at].double().numpy(), T, HALF[dtype])
+    for out, grad in ((f, dl), (fused, fused["dlogits"])):
+        for k in ("loss", "lse", "p_rest"):
+            close(out[k][at.to(DEV)], o[k], tol[k], k)
+        close(grad[0, at.to(DEV)], o["dlogits"], tol["dlogits"], "dlogits")
+    # every row: the fused and the separate passes agree (two sums, each within its bound of the row)
+    big = fused["dlogits"][0].float().abs().amax(1, keepdim=True).clamp(min=1e-30)
+    assert bool(((fused["dlogits"][0].float() - dl[0].float()).abs() <= big * (4 * HALF[dtype] + 2e-4)).all())
+    assert bool(((fused["loss"] - f["loss"]).abs() <= 1e-4 * (1 + f["loss"].abs())).all())
+
+
 @pytest.mark.parametrize("beta,tail", WAYS)
 def test_confident_students(beta, tail):
     """The list holds all but a sliver of the student's mass, or nearly none of it."""
