@@ -161,14 +161,19 @@ __device__ __forceinline__ float rest_ratio(float q, float p, float d) {
 }
 
 // The unlisted columns' gradient g F p_j as f 2^((x_j - x0) c), from p_j = 2^((x_j - x0) c) scale.
-// Where the student leaves the rest next to nothing, F is of the order of 1 / p_rest: the power of two
-// in p_rest moves from f into x0, so that neither f nor the exponentials leave fp32's range.
+// Where the factor is large (F is of the order of 1 / p_rest where the student leaves the rest next to
+// nothing), its power of two moves into x0: neither f nor the exponentials then leave fp32's range
+// before their product does.
 struct Stream {
   float f, x0;
 };
-__device__ __forceinline__ Stream stream_of(float g, float F, float scale, float x0, float p_rest, float T) {
-  const float lift = p_rest > 0.f && p_rest < 0x1p-30f ? floorf(-log2f(p_rest)) : 0.f;
-  return Stream{g * (F * exp2f(-lift) * scale), x0 - lift * kLn2 * T};
+__device__ __forceinline__ Stream stream_of(float g, float F, float scale, float x0, const DistillParams& p) {
+  const float lift = rintf(log2f(fabsf(F)) + log2f(scale) + log2f(fabsf(g)));
+  if (!(lift > 0.f)) return Stream{g * (F * scale), x0};
+  const float x1 = x0 - fminf(lift, 240.f) * kLn2 * p.T;
+  const Scaled z = over_T(x1 - x0, p);  // 2^-lift, as x1 is rounded
+  const float down = expf(0.5f * z.hi);
+  return Stream{g * (F * down * scale) * (down * (1.f + z.lo)), x1};
 }
 
 // One row's results (every lane of the list warp); the slots then hold G_k and p_k.
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
     if (FUSED) {
       for (int k = lane; k < K; k += 32) sl.lq[k] = bad ? nan : g * (sl.lq[k] - sl.x[k] * o.S);
       if (lane == 0) {
-        const Stream t = stream_of(g, o.F_rest - o.S, o.inv_s, o.m, o.p_rest, p.T);
+        const Stream t = stream_of(g, o.F_rest - o.S, o.inv_s, o.m, p);
         sh_factor = g == 0.f ? 0.f : (bad ? nan : t.f);
         sh_m = t.x0;
         sh_stat[0].s = g;
@@ -601,8 +606,7 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
     if (lane == 0) {
       const float x0 = lse * p.T;
       const Scaled z = over_T(x0, p);
-      const Stream st = stream_of(g, (p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum, expf((z.hi - lse) + z.lo), x0, p_rest,
-                                  p.T);
+      const Stream st = stream_of(g, (p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum, expf((z.hi - lse) + z.lo), x0, p);
       sh_factor = st.f;
       sh_x0 = st.x0;
     }
