@@ -168,7 +168,7 @@ struct Stream {
   float f, x0;
 };
 __device__ __forceinline__ Stream stream_of(float g, float F, float scale, float x0, const DistillParams& p) {
-  const float lift = rintf(log2f(fabsf(F)) + log2f(scale) + log2f(fabsf(g)));
+  const float lift = ceilf(log2f(fabsf(F)) + log2f(scale) + log2f(fabsf(g)) + 0.01f);  // leaves |f| <= 1
   if (!(lift > 0.f)) return Stream{g * (F * scale), x0};
   const float x1 = x0 - fminf(lift, 240.f) * kLn2 * p.T;
   const Scaled z = over_T(x1 - x0, p);  // 2^-lift, as x1 is rounded
