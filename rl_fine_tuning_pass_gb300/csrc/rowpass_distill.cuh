@@ -686,13 +686,14 @@ cudaError_t launch_distill_bwd_t(bool same_phase, const DistillParams& p, int64_
 }
 
 // Long rows with eight vectors in flight per thread (8192 rows of 304 KB: 662 us against 673 us); few
-// rows in parts, a CTA each.
+// rows in parts, a CTA each, unless the gradients go over the logits: every part reads all of the row's
+// listed logits, which another part may have overwritten by then.
 template <class E>
 cudaError_t launch_distill_bwd_e(bool same_phase, const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
   const int64_t bytes = static_cast<int64_t>(p.x.V) * sizeof(typename E::storage);
   if (pick_threads_bwd(p.x.V, sizeof(typename E::storage), rows, sms) == 64)
     return launch_distill_bwd_t<E, 64, kUnroll>(same_phase, p, rows, 1, s);
-  const int parts = row_parts<E>(p, rows, 5LL * sms);
+  const int parts = p.dx.ptr == p.x.ptr ? 1 : row_parts<E>(p, rows, 5LL * sms);
   return bytes / parts < 131072 ? launch_distill_bwd_t<E, 256, kUnroll>(same_phase, p, rows, parts, s)
                                 : launch_distill_bwd_t<E, 256, 8>(same_phase, p, rows, parts, s);
 }

@@ -324,6 +324,23 @@ def test_autograd_against_the_oracle_and_differences():
         g.sum().backward()
 
 
+@pytest.mark.parametrize("dtype,V", [(torch.float32, 100003), (torch.bfloat16, 151936)])
+@pytest.mark.parametrize("R", [1, 3, 40, 200])
+def test_few_rows_in_place(R, V, dtype):
+    # a row that several CTAs would share: none may read a listed logit that another has overwritten
+    x = (randn(1, R, V, seed=R) * 2).to(dtype).to(DEV)
+    ids, lp, _ = rp.topk_log_softmax(x, 256)
+    lp = (lp - 0.5).contiguous()
+    w = randn(R, seed=3).to(DEV)
+    how = dict(T=0.9, beta=0.3, tail=True)
+    f = rp.distill_topk_fwd(x, ids, lp, **how)
+    want = rp.distill_topk_bwd(x, ids, lp, w, f["lse"], f["p_rest"], **how)
+    for _ in range(20):
+        y = x.clone()
+        rp.distill_topk_bwd(y, ids, lp, w, f["lse"], f["p_rest"], **how, dlogits=y)
+        same_bits(y, want, "dlogits")
+
+
 def test_captured_and_replayed():
     x = (randn(2, 5, 3001, seed=1) * 2).to(torch.bfloat16)
     ids, lp = (t.to(DEV) for t in teacher(x, 20, 2))
