@@ -13,6 +13,11 @@ library's entry points.  Marshalling only: every step runs in the CUDA kernels.
 Gradients flow to ``logits`` only (the other inputs are treated as constants, as in GRPO).
 The backward of ``grpo_loss`` receives d(objective)/d(loss_r) per token from autograd, which
 is exactly the per-token ``dloss`` of grpo_loss_bwd.
+
+Forward and backward may be captured together into a CUDA graph.  While another graph of
+autograd's that was built on another stream keeps a leaf's gradient node alive, torch refuses to
+capture a backward of that leaf, for its own operators too; drop it first, or call the
+``_fwd`` and ``_bwd`` entry points, which involve no autograd.
 """
 
 from __future__ import annotations

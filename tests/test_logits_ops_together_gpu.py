@@ -83,3 +83,29 @@ def test_a_decode_step():
     assert ids[2, 0] == 4000 and abs(float(logp[2, 0])) < 1e-6 and float(logp[2, 1]) == float("-inf")
     lp, lse2 = rl.selective_log_softmax_fwd(x, ids[:, 0].contiguous(), T=1.0)
     assert bool(((lp - logp[:, 0]).abs() <= 1e-5).all())
+
+
+def test_gradients_captured_and_replayed():
+    B, L, V, K, N = 2, 5, 1003, 12, 9
+    x = (randn(B, L, V, seed=1) * 2).to(DEV).requires_grad_(True)
+    tokens = torch.from_numpy(np.random.default_rng(2).integers(0, V, (B, N))).to(DEV)
+    rep = torch.tensor([1.3, 0.8], device=DEV)
+    ids, tlp, _ = rl.topk_log_softmax(x.detach(), K)
+
+    def step():
+        y = rl.process_logits(x, tokens=tokens, repetition=rep)
+        div, _ = rl.distill_topk_loss(y, ids, tlp, beta=0.5, tail=True)
+        return torch.autograd.grad(div.sum(), x)[0]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for n in range(2):
+        with torch.no_grad():
+            x.copy_(randn(B, L, V, seed=20 + n))
+        graph.replay()
+        assert torch.equal(got, step())
