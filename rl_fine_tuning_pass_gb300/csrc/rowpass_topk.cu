@@ -1,30 +1,25 @@
 // The K largest log-probs of each row, log_softmax(x / T), with their columns: sorted, ties
 // to the lowest column.
 //
-// One sweep over the row forms the softmax statistic (logits_stat.cuh) and notes where candidates
-// are.  Each thread keeps the largest element it has met in the even and in the odd places of its
+// One sweep over the row forms the softmax statistic (logits_stat.cuh) and notes the largest element
+// of every chunk (the vectors of one thread in one step; in rows past kNotes chunks of several steps).
+// Each thread also keeps the largest element it has met in the even and in the odd places of its
 // vectors, 512 maxima per CTA (up to K = 64 one of both, 256); the K-th largest of those maxima is a
-// lower bound of the K-th largest element seen so far (K different elements reach it), so a chunk
-// (the vectors of one thread in one step) without an element that reaches it cannot hold a result.
-// The bound is taken anew after 1, 4, 16, ... steps of the sweep and at its end: of N(0, 1) elements
-// about 64 chunks of the first step reach it at K = 64, and three times as many of each quadrupling,
-// some 460 of a row of 151936 (a bound after each doubling notes fewer chunks and waits at more
-// barriers: 2048 rows of 32000 at K = 128 took 62 us, against 59 us).  The chunks that also reach the
-// last bound (about 64) are listed and read again, and their elements that reach it (about 70) are
-// ranked (rank_entries).  With few rows, where a CTA's part is a few steps, all its chunks are noted and
-// the bound is taken once, at the end.
+// lower bound of the K-th largest element (K different elements reach it), so a chunk without an
+// element that reaches it cannot hold a result.  The chunks that do (about 70 of a row of N(0, 1)
+// elements at K = 64) are listed and read again, and their elements that reach the bound (about 74)
+// are ranked (rank_entries).  Noting only the chunks that reach a bound taken again and again within
+// the sweep waits at more barriers: 2048 rows of 32000 bf16 at K = 128 took 50 us, against 43 us.
 //
-// Measured: the top 64 of 8192 rows of 151936 bf16 take 423 us (5.9 TB/s, 87% of the copy rate; radix
-// selection alone took 4.2 ms), of which the DRAM reads are 1.07 times the row; what is left are the
-// barriers of the bounds and of the ranking, which five CTAs per SM do not hide whole.
+// Measured: the top 64 of 8192 rows of 151936 bf16 take 394 us (6.3 TB/s, 93% of the copy rate; radix
+// selection alone took 4.2 ms); what is left are the barriers of the bound and of the
+// ranking, which five CTAs per SM do not hide whole.
 //
-// Rows that collect more than the buffers hold (thousands of ties at the K-th value, large
-// values that come last) are done again by radix selection on order-preserving keys.
+// Rows that collect more than the buffers hold (thousands of ties at the K-th value) are done
+// again by radix selection on order-preserving keys.
 //
 // With few rows, a cluster of CTAs takes a row: each CTA ranks its own part, the first one
 // merges the sorted lists and the statistics, which the others write into its shared memory.
-#include <climits>
-
 #include "logits_ops.h"
 #include "logits_stat.cuh"
 
@@ -154,6 +149,7 @@ __device__ void radix_select(const typename E::storage* row, int V, int K, uint6
 constexpr int kMaxima = 2 * kTopkThreads;   // running maxima per CTA
 constexpr int kOneMaximum = 64;             // up to this K one maximum per thread is enough
 constexpr int kSurvivors = 1024;            // entries that are ranked
+constexpr int kNotes = 8192;                // chunks whose largest element is noted
 constexpr uint32_t kKeyNegInf = 0x007Fu;    // high half of the key of -inf
 
 // A lower bound of the K-th largest of the CTA's running maxima (high halves of their keys in sh;
@@ -195,8 +191,8 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t cluster_addr, uint64_t v
 // 256 buckets by their distance from `least` (its exponent and three bits: the top of a row thins
 // out with the distance), larger ones first; a place is what the larger buckets hold, and what is
 // larger in the entry's own.  Up to 96 entries are counted straight away, which is as fast as the
-// buckets' barriers there: the top 64 (about 70 entries) of 2000 rows of 32000 take 39.6 us counted
-// and 40.3 us with buckets, the top 128 take 52.7 us and 49.1 us, the top 256 109 us and 72 us.
+// buckets' barriers there: the top 64 (about 70 entries) of 2000 rows of 32000 took 39.6 us counted
+// and 40.3 us with buckets, the top 128 52.7 us and 49.1 us, the top 256 109 us and 72 us.
 template <class E, int T, class F>
 __device__ __forceinline__ void rank_entries(const uint64_t* surv, int m, uint32_t least, uint64_t* sorted,
                                              unsigned (&first)[256], F put) {
@@ -260,18 +256,19 @@ struct TopkPart {  // what one CTA of a cluster hands to the first
 // CS CTAs per row (a cluster when CS > 1).  Dynamic shared memory: cap candidates, then
 // kSurvivors, then (CS > 1) the CTAs' lists.
 template <class E, int CS>
-__global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams p, int cap) {
+__global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams p, int notes, int gs) {
   using S = typename E::storage;
   constexpr int VEC = E::kVec, T = kTopkThreads, U = kUnroll;
   extern __shared__ uint64_t topk_smem[];
   __shared__ uint16_t maxima[kMaxima];
   __shared__ uint64_t list[kTopkMax];
   __shared__ TopkPart parts[CS];
-  __shared__ float sh_thr;
-  __shared__ unsigned sh_n, sh_m, sh_c;
+  __shared__ uint32_t sh_least;
+  __shared__ unsigned sh_m, sh_c;
   __shared__ unsigned buckets[256];
-  uint64_t* cand = topk_smem;  // chunks: the largest element's key, and the first vector
-  uint64_t* surv = topk_smem + cap;
+  // the chunks' largest elements, then room for rank_entries
+  float* noted = reinterpret_cast<float*>(topk_smem);
+  uint64_t* surv = topk_smem + notes / 2;
   uint64_t* lists = surv + kSurvivors;
   if (CS > 1) cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
   wait_for_previous_grids();
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   const RowSplit sp = split_row<E>(row, V);
   const int part = (sp.nvec + CS - 1) / CS;
   const int v0 = min(sp.nvec, static_cast<int>(rank) * part), v1 = min(sp.nvec, v0 + part);
-  if (tid == 0) sh_n = sh_m = sh_c = 0u;
+  if (tid == 0) sh_m = sh_c = 0u;
   __syncthreads();
 
   MaxRun rs;
@@ -304,51 +301,38 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     sub.x = fmaxf(sub.x, edge);
   }
 
-  float thr = -INFINITY;
-  auto bound = [&]() {  // a new bound from the maxima so far
-    if (K <= kOneMaximum) {
-      maxima[tid] = static_cast<uint16_t>(key_of(fmaxf(sub.x, sub.y)) >> 16);
-    } else {
-      maxima[tid] = static_cast<uint16_t>(key_of(sub.x) >> 16);
-      maxima[T + tid] = static_cast<uint16_t>(key_of(sub.y) >> 16);
-    }
-    __syncthreads();
-    if (tid < 32) {
-      const uint32_t k = kth_maximum(maxima, K);
-      if (tid == 0) sh_thr = k <= kKeyNegInf ? -INFINITY : value_of(k << 16);
-    }
-    __syncthreads();
-    thr = sh_thr;
-  };
   const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
-  const bool all = CS > 1 && (v1 - v0 + U * T - 1) / (U * T) * T <= cap;  // every chunk fits
-  int step = 0, next = all ? INT_MAX : 1;
-  auto fold = [&](const uint4 (&v)[U], int i) {
+  int step = 0;           // steps done
+  float top = -INFINITY;  // of a chunk of several steps
+  auto note = [&]() {
+    noted[((step - 1) >> gs) * T + tid] = top;
+    top = -INFINITY;
+  };
+  auto fold = [&](const uint4 (&v)[U]) {
     const float2 pm = maxrun_vectors<E>(rs, v, c);
     sub.x = fmaxf(sub.x, pm.x);
     sub.y = fmaxf(sub.y, pm.y);
-    if (++step == next) {
-      bound();
-      next *= 4;
-    }
     const float m = fmaxf(pm.x, pm.y);
-    if (all) {
-      cand[(step - 1) * T + tid] = static_cast<uint64_t>(key_of(m)) << 32 | static_cast<uint32_t>(i);
-    } else if (m >= thr && m > -INFINITY) {
-      const unsigned at = atomicAdd(&sh_n, 1u);
-      if (at < static_cast<unsigned>(cap)) cand[at] = static_cast<uint64_t>(key_of(m)) << 32 | static_cast<uint32_t>(i);
+    ++step;
+    if (gs == 0) {  // chunks of one step (with the general form alone 2048 rows of 32000 fp32 take 48 us, not 42)
+      noted[(step - 1) * T + tid] = m;
+      return;
     }
+    top = fmaxf(top, m);
+    if ((step & ((1 << gs) - 1)) == 0) note();
   };
   int i0 = v0;
   for (; i0 + U * T <= v1; i0 += U * T) {
     uint4 v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) v[k] = ld_nc_v4(vb + i0 + k * T + tid);
-    if (tid == 0 && i0 + U * T < v1)  // ask L2 for the next step (8192 rows of 304 KB: 445 us against 462 us)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(vb + i0 + U * T),
-                   "r"(static_cast<uint32_t>(min(v1 - i0 - U * T, U * T)) * 16u)
-                   : "memory");
-    fold(v, i0 + tid);
+    if (tid == 0) {  // ask L2 for the step after the next (2000 rows of 304 KB: 110 us; the next step: 113 us)
+      const int a = i0 == v0 ? i0 + U * T : i0 + 2 * U * T, n = min(v1, i0 + 3 * U * T) - a;
+      if (n > 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(vb + a), "r"(static_cast<uint32_t>(n) * 16u)
+                     : "memory");
+    }
+    fold(v);
   }
   if (i0 < v1) {
     const uint32_t pad = sizeof(S) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
@@ -358,45 +342,59 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
       v[k] = make_uint4(pad, pad, pad, pad);
       if (i0 + k * T + tid < v1) v[k] = ld_nc_v4(vb + i0 + k * T + tid);
     }
-    fold(v, i0 + tid);
+    fold(v);
   }
-  if (all || step * 4 != next) bound();  // elements since the last bound
+  if ((step & ((1 << gs) - 1)) != 0) note();
+
+  // the bound
+  if (K <= kOneMaximum) {
+    maxima[tid] = static_cast<uint16_t>(key_of(fmaxf(sub.x, sub.y)) >> 16);
+  } else {
+    maxima[tid] = static_cast<uint16_t>(key_of(sub.x) >> 16);
+    maxima[T + tid] = static_cast<uint16_t>(key_of(sub.y) >> 16);
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const uint32_t k = kth_maximum(maxima, K);
+    if (tid == 0) sh_least = (k <= kKeyNegInf ? kKeyNegInf + 1u : k) << 16;  // an element above -inf at least
+  }
   MaxStat st = maxstat_block<T>(rs.stat(), c);
   __syncthreads();
 
-  // the noted chunks that reach the last bound, then their elements that do, four threads to a chunk
-  const unsigned n = all ? static_cast<unsigned>(step * T) : sh_n;
-  const uint32_t least = key_of(thr);
+  // the chunks that reach it, then their elements that do, four threads to a chunk and step
+  const uint32_t least = sh_least;
+  const float thr = value_of(least);
+  const int n = ((step + (1 << gs) - 1) >> gs) * T;
   constexpr unsigned kChunks = 2 * kTopkMax;
   uint32_t* chunks = reinterpret_cast<uint32_t*>(list);
-  for (unsigned q = tid; q < min(n, static_cast<unsigned>(cap)); q += T) {
-    const uint64_t e = cand[q];
-    if (static_cast<uint32_t>(e >> 32) < least || static_cast<uint32_t>(e >> 32) <= key_of(-INFINITY)) continue;
+  for (int q = tid; q < n; q += T) {
+    if (!(noted[q] >= thr)) continue;
     const unsigned at = atomicAdd(&sh_c, 1u);
-    if (at < kChunks) chunks[at] = static_cast<uint32_t>(e);
+    if (at < kChunks) chunks[at] = static_cast<uint32_t>(q);
   }
   __syncthreads();
   const unsigned nc = sh_c;
-  if (edge > -INFINITY && edge >= thr) take(edge, edge_j);
-  for (unsigned q = tid; q < U * min(nc, kChunks); q += T) {
-    const int i = static_cast<int>(chunks[q / U]) + static_cast<int>(q % U) * T;
+  if (edge_j >= 0 && edge >= thr) take(edge, edge_j);
+  for (unsigned q = tid; q < U * min(nc, kChunks) << gs; q += T) {
+    const unsigned at = q / U >> gs, chunk = chunks[at], in = (q / U) - (at << gs);
+    const int i = v0 + static_cast<int>(((chunk / T << gs) + in) * U + q % U) * T + static_cast<int>(chunk % T);
     if (i >= v1) continue;
     float f[VEC];
     E::unpack(ld_nc_v4(vb + i), f);
 #pragma unroll
     for (int k = 0; k < VEC; ++k)
-      if (f[k] >= thr && f[k] > -INFINITY) take(f[k], sp.head + i * VEC + k);
+      if (f[k] >= thr) take(f[k], sp.head + i * VEC + k);
   }
   __syncthreads();
   int m = static_cast<int>(sh_m);
-  const bool over = n > static_cast<unsigned>(cap) || nc > kChunks || m > kSurvivors;
+  const bool over = nc > kChunks || m > kSurvivors;
   uint64_t* mine = list;
   if (CS > 1) {
     cluster_wait();
     // this CTA's sorted list, in the first CTA's shared memory
     const uint32_t at = map_to_rank(smem_addr(lists + rank * static_cast<uint32_t>(K)), 0);
     if (!over)
-      rank_entries<E, T>(surv, m, least, cand, buckets, [&](int place, uint64_t e) {
+      rank_entries<E, T>(surv, m, least, topk_smem, buckets, [&](int place, uint64_t e) {
         if (place < K) st_cluster_u64(at + 8u * place, e);
       });
     if (tid == 0) {
@@ -461,7 +459,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
     for (int k = tid; k < K - have; k += T) put(have + k, mine[k]);
   }
   if (CS == 1) {
-    rank_entries<E, T>(surv, m, least, cand, buckets, [&](int place, uint64_t e) {
+    rank_entries<E, T>(surv, m, least, topk_smem, buckets, [&](int place, uint64_t e) {
       if (place < K) put(place, e);
     });
   } else {
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
       int place = at;
       int lo[CS] = {};
 #pragma unroll 1
-      for (int step = kTopkMax / 2; step > 0; step >>= 1) {  // how many of list q are larger; the lists' searches overlap
+      for (int step = kTopkMax / 2; step > 0; step >>= 1) {  // how many of each list are larger, side by side
 #pragma unroll
         for (int q = 0; q < CS; ++q)
           if (lo[q] + step <= parts[q].n && lists[q * K + lo[q] + step - 1] > e) lo[q] += step;
@@ -499,11 +497,17 @@ int pick_split(const TopkParams& p, int64_t rows, int sms) {
 
 template <class E, int CS>
 cudaError_t launch_topk_cs(const TopkParams& p, int64_t rows, cudaStream_t s) {
-  const int cap = p.K > 128 ? 4096 : 2048;
-  const size_t smem = 8 * (static_cast<size_t>(cap) + kSurvivors + (CS > 1 ? CS * p.K : 0));
+  // chunks of 2^gs steps
+  const int vecs = p.x.V / E::kVec / CS + 1;
+  const int64_t steps = (static_cast<int64_t>(vecs) + kTopkThreads * kUnroll - 1) / (kTopkThreads * kUnroll);
+  int gs = 0;
+  while (((steps + (1LL << gs) - 1) >> gs) * kTopkThreads > kNotes) ++gs;
+  const int least = 2 * kSurvivors;  // rank_entries sorts as many entries there
+  const int n = static_cast<int>((steps + (1LL << gs) - 1) >> gs) * kTopkThreads, notes = n < least ? least : n;
+  const size_t smem = 4 * static_cast<size_t>(notes) + 8 * (kSurvivors + (CS > 1 ? CS * p.K : 0));
   if (smem > 40 * 1024) {  // with the static part past the 48 KB that need no leave
     const cudaError_t e = cudaFuncSetAttribute(topk_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               8 * (4096 + kSurvivors + (CS > 1 ? CS * kTopkMax : 0)));
+                                               4 * kNotes + 8 * (kSurvivors + (CS > 1 ? CS * kTopkMax : 0)));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -519,7 +523,7 @@ cudaError_t launch_topk_cs(const TopkParams& p, int64_t rows, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CS > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, topk_kernel<E, CS>, p, cap);
+  return cudaLaunchKernelEx(&cfg, topk_kernel<E, CS>, p, notes, gs);
 }
 
 template <class E>

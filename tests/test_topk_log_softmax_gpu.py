@@ -106,6 +106,22 @@ def test_hard_rows_among_many():
         close(logp[at], o_logp, 1e-5 + 1e-5 * np.abs(o_logp), "logp")
 
 
+@pytest.mark.parametrize("R,V,dtype", [(400, 140003, torch.float32), (310, 600011, torch.bfloat16),
+                                       (1, 2200003, torch.float32), (2, 2200003, torch.bfloat16)])
+@pytest.mark.parametrize("K", [7, 200])
+def test_rows_whose_chunks_are_several_steps(R, V, dtype, K):
+    # the row as a whole, and (few rows) the parts of a cluster
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = (torch.randn(R, V, generator=g, device=DEV) * 3).to(dtype)
+    x[0] = torch.arange(V, device=DEV) / 64    # rising: the largest come last, in one thread's chunks or a few
+    ids, logp, lse = rp.topk_log_softmax(x, K)
+    for r in {0, R // 2, R - 1}:
+        o_ids, o_logp, o_lse = lo.topk_log_softmax(f64(x[r:r + 1]), K, 1.0)
+        assert np.array_equal(ids[r:r + 1].cpu().numpy(), o_ids)
+        close(logp[r:r + 1], o_logp, 1e-5 + 1e-5 * np.abs(o_logp), "logp")
+        close(lse[r:r + 1], o_lse, 1e-5 + 1e-5 * np.abs(o_lse), "lse")
+
+
 def test_rows_without_log_probs():
     """NaN, +inf, all -inf: ids 0..K-1 and NaN log-probs; the lse says why."""
     x = randn(1, 6, 500, seed=1)
