@@ -544,7 +544,9 @@ grpo_status topk_log_softmax(const grpo_rows* logits, int64_t K, float T, int64_
  *            KL(q | p) at beta = 0;  KL(p | q) at beta = 1
  *   tail == 0: q_k is renormalised over the list (any shift of teacher_logp gives the same),
  *              q_rest = 0;  beta must be < 1
- *   tail != 0: q_k = exp(teacher_logp_k), q_rest = max(1 - sum q_k, 2^-20)
+ *   tail != 0: q_k = exp(teacher_logp_k), q_rest = max(1 - sum q_k, 2^-20).  A row without a
+ *              rest (every unlisted logit is -inf, or every column is listed) is taken as with
+ *              tail == 0: the teacher renormalised over its list
  *   with G_b = p_b dloss/dp_b and S = sum_b G_b:
  *   dlogits_rj = (dloss_r / T) (G_k - p_j S) at a listed column,
  *                (dloss_r / T) p_j (G_rest / p_rest - S) at the others
@@ -555,8 +557,9 @@ grpo_status topk_log_softmax(const grpo_rows* logits, int64_t K, float T, int64_
  *   teacher_logp  [B*L][K] fp32 (of unused slots not used)
  *   mask          [B*L] uint8 or NULL: masked rows write +0.0 to every output, read no logits
  *   loss, lse     [B*L] fp32 outputs;  p_rest: [B*L] fp32, the student's mass outside the list:
- *                 the sum of exp(x_j / T - lse) over those columns, with the lse as stored (lse
- *                 and p_rest are what the backward needs)
+ *                 the sum of exp(x_j / T - lse) over those columns, with the lse as stored, and
+ *                 held at 2^-149 or more: 0 only where there is no rest (lse and p_rest are what
+ *                 the backward needs)
  *   dloss         [B*L] fp32 upstream gradient of each row's loss
  *   dlogits       as in grpo_loss_bwd (may alias logits exactly).  Rows that are masked or
  *                 whose dloss_r / T is 0.0 are written as +0.0 without reading their logits

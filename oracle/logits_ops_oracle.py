@@ -137,7 +137,8 @@ def distill_topk(x, ids, tlogp, T, beta, tail, mask=None, dloss=None):
         inside = np.zeros(V, bool)
         inside[at] = True
         q = np.exp(lq)
-        if tail:
+        # without a column that has any mass outside the list there is no rest, as without the tail
+        if tail and not np.all(np.isneginf(x[r][~inside])):
             q_rest = max(1.0 - q.sum(), REST_MIN)
         else:
             q, q_rest = (q / q.sum() if len(q) else q), 0.0

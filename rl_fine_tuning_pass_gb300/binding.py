@@ -629,8 +629,8 @@ def distill_topk_fwd(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, 
     """Divergence of each row's softmax(logits / T) from a teacher's top log-probs (ids and
     teacher_logp [B*L, K], K <= 256): dict with loss, lse and p_rest, each [B*L] fp32.
     beta 0: KL(teacher | student), 1: KL(student | teacher), between: the mixture's.  tail:
-    the teacher's mass outside its list is one more bucket (needed at beta 1); without it the
-    teacher is renormalised over the list."""
+    the teacher's mass outside its list is one more bucket (needed at beta 1); without it, and in
+    rows whose unlisted logits are all -inf, the teacher is renormalised over the list."""
     x, B, L, _ = _pack_rows(logits)
     R, dev = B * L, logits.device
     pi, pt, K = _list_of(ids, teacher_logp, R, dev)

@@ -12,7 +12,8 @@
 // of rowgrad_kernel with one factor per row, and K elements written after it.  p_rest is summed
 // from the columns outside the list (a bitmap in shared memory leaves the listed ones out of the
 // stream), not taken from 1 - sum p_k: it keeps its relative accuracy when the list holds nearly all
-// of the mass.
+// of the mass.  Where no unlisted column has any (they are all -inf, or there are none), there is
+// no rest: the row is taken as without the tail, its teacher renormalised over the list.
 //
 // Bound by HBM: 8192 rows of 151936 bf16, a quarter of them masked, take 279 us forward (6.7 TB/s),
 // 662 us backward (6.6 TB/s, reads and writes), 818 us fused.
@@ -34,6 +35,7 @@ namespace {
 
 constexpr int kBitmapBytes = 32768;      // 262144 columns; beyond, positions wrap and are checked
 constexpr double kRestMin = 0x1p-20;     // least teacher mass outside the list
+constexpr float kLeastMass = 0x1p-149f;  // p_rest of a rest whose mass underflows: 0 says that there is none
 
 // The list of one row in shared memory.  id -1: an unused slot.
 struct Slots {
@@ -117,13 +119,13 @@ __device__ __forceinline__ float exp_over_T(float d, const DistillParams& p) {
 }
 
 // What the teacher's list says (one warp): log q_k = lq_k - shift, the mass of the list and
-// outside it, and sum q - 1.
+// outside it, sum q - 1, and (tail) the shift that renormalises it.
 struct Teacher {
-  float shift, list, rest, over;
+  float shift, list, rest, over, log_list;
 };
 __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) {
   const int lane = threadIdx.x & 31;
-  Teacher t{0.f, 1.f, 0.f, 0.f};
+  Teacher t{0.f, 1.f, 0.f, 0.f, 0.f};
   if (tail) {
     double sum = 0.0;
     for (int k = lane; k < K; k += 32)
@@ -133,6 +135,7 @@ __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) 
     t.list = static_cast<float>(sum);
     t.rest = static_cast<float>(rest);
     t.over = static_cast<float>(rest - left);
+    t.log_list = static_cast<float>(log(sum));
   } else {
     float m = -INFINITY;
     for (int k = lane; k < K; k += 32)
@@ -218,6 +221,7 @@ __device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const Te
   // relative to the lse as it is stored: the backward's other p_j are too, and the common factor
   // cancels in its differences
   o.p_rest = s_rest * expf((zm.hi - o.lse) + zm.lo);
+  if (o.p_rest == 0.f && st.s != 0.f) o.p_rest = kLeastMass;
   o.loss = row_loss(warp_sum(loss) + t.loss, te.over, p.beta);
   o.m = m;
   o.inv_s = inv_s;
@@ -516,6 +520,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
     const MaxStat* stats = CS > 1 ? sh_parts : sh_stat;
     const MaxStat st = maxstat_warp(lane < kStats ? stats[lane] : MaxStat{-FLT_MAX, 0.f}, c);
     const float g = FUSED ? p.dloss[r] / p.T : 0.f;
+    if (p.tail && st.s == 0.f) te = Teacher{te.log_list, 1.f, 0.f, 0.f, 0.f};  // there is no rest
     const RowResult o = finish_row(sl, K, te, st, p);
     const float nan = __int_as_float(0x7FC00000);
     bad = __any_sync(0xFFFFFFFFu, bad);
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
     const float lse = p.lse[r], p_rest = p.p_rest[r];
     load_slots<E>(sl, p, r, row);
     __syncwarp();
-    const Teacher te = teacher_of(sl, K, p.tail);
+    const Teacher te = teacher_of(sl, K, p.tail && p_rest != 0.f);
     float S_sum = 0.f;
     for (int k = lane; k < K; k += 32) {
       if (sl.id[k] < 0) continue;
