@@ -105,10 +105,16 @@ def topk_log_softmax(x, K, T):
     return ids, logp, lse
 
 
-def _kl(a, b):
+def _kl(a, log_a, log_b):
     """a log(a / b) per bucket, 0 where a is 0."""
-    with np.errstate(divide="ignore", invalid="ignore"):
-        return np.where(a == 0, 0.0, a * (np.log(a) - np.log(b)))
+    with np.errstate(invalid="ignore"):
+        return np.where(a == 0, 0.0, a * (log_a - log_b))
+
+
+def _log_sum(z):
+    """log sum exp(z), -inf of nothing."""
+    m = z.max() if len(z) else -np.inf
+    return m if np.isneginf(m) else m + np.log(np.exp(z - m).sum())
 
 
 def distill_topk(x, ids, tlogp, T, beta, tail, mask=None, dloss=None):
@@ -143,15 +149,18 @@ def distill_topk(x, ids, tlogp, T, beta, tail, mask=None, dloss=None):
         else:
             q, q_rest = (q / q.sum() if len(q) else q), 0.0
         P, Q = np.append(p[at], p[~inside].sum()), np.append(q, q_rest)
+        # log-probs of the buckets from the logits: a mass may be less than 64 bits hold
+        rest = _log_sum(z[~inside])
         with np.errstate(divide="ignore", invalid="ignore"):
+            LP, LQ = np.append(z[at], rest) - lse, np.log(Q)
             if beta == 0.0:
-                terms, slope = _kl(Q, P), -Q / P
+                terms, slope = _kl(Q, LQ, LP), None
             elif beta == 1.0:
-                terms, slope = _kl(P, Q), np.log(P / Q) + 1.0
+                terms, slope = _kl(P, LP, LQ), LP - LQ + 1.0
             else:
-                M = beta * Q + (1.0 - beta) * P
-                terms = beta * _kl(Q, M) + (1.0 - beta) * _kl(P, M)
-                slope = (1.0 - beta) * np.log(P / M)
+                LM = np.logaddexp(np.log(beta) + LQ, np.log1p(-beta) + LP)
+                terms = beta * _kl(Q, LQ, LM) + (1.0 - beta) * _kl(P, LP, LM)
+                slope = (1.0 - beta) * (LP - LM)
         # G = p dL/dp: at p = 0 the limit, -q for the forward divergence and 0 for the others
         G = -Q if beta == 0.0 else np.where(P == 0, 0.0, P * np.where(P == 0, 0.0, slope))
         S = G.sum()
@@ -159,7 +168,9 @@ def distill_topk(x, ids, tlogp, T, beta, tail, mask=None, dloss=None):
         out["loss"][r], out["lse"][r], out["p_rest"][r] = terms.sum(), lse, P[-1]
         out["G"][r], out["terms"][r], out["F"][r] = np.abs(G).sum() + abs(S), np.abs(terms).sum(), abs(F)
         if dloss is not None:
-            d = p * (F - S)
+            # p_j G_rest / p_rest with p_j / p_rest from the logits
+            with np.errstate(invalid="ignore", over="ignore"):   # of listed columns, set below
+                d = (np.exp(z - rest) * G[-1] if rest > -np.inf else 0.0) - p * S
             d[at] = G[:-1] - p[at] * S
             out["dlogits"][r] = d * (float(dloss[r]) / T)
     return out

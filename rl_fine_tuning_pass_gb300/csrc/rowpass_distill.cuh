@@ -14,6 +14,10 @@
 // stream), not taken from 1 - sum p_k: it keeps its relative accuracy when the list holds nearly all
 // of the mass.  Where no unlisted column has any (they are all -inf, or there are none), there is
 // no rest: the row is taken as without the tail, its teacher renormalised over the list.
+// A rest of less mass than fp32's normal numbers hold ("faint": the list is 87 T or more above it) is
+// kept as its statistic: its log-ratio comes from log s and the maxima, and the unlisted columns'
+// gradient at beta = 0, -g q_rest p_j / p_rest, from 2^((x_j - m_rest) c) / s_rest.  The backward, which
+// has p_rest alone, sweeps such a row once more for that statistic (rest_stat).
 //
 // Bound by HBM: 8192 rows of 151936 bf16, a quarter of them masked, take 279 us forward (6.7 TB/s),
 // 662 us backward (6.6 TB/s, reads and writes), 818 us fused.
@@ -55,8 +59,9 @@ __device__ __forceinline__ Slots slots_at(void* at, int K) {
 // precision where p and q are near each other.  The parts of the loss carry (p - q) or (q - p)
 // besides (they sum to nothing over the buckets, `row_loss` takes out what is left): an error of
 // r then enters times p - q, so one that all buckets share, such as that of log s, does not count.
+// F = G / p (at beta = 0 that of q = 0).
 struct Term {
-  float loss, G;
+  float loss, G, F;
 };
 __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
   Term t;
@@ -64,9 +69,11 @@ __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
     const bool near = fabsf(r) < 0.5f;
     const float e = expm1f(near ? r : 0.f);
     t.G = near ? -p * e : p - q;  // p (1 - q / p)
+    t.F = 1.f;
     t.loss = q == 0.f ? p : (near ? q * (expm1f(-r) + r) : q * r - q + p);
   } else if (beta == 1.f) {
     const bool near = fabsf(r) < 0.5f;
+    t.F = -r;
     t.G = p == 0.f ? 0.f : -p * r;
     t.loss = p == 0.f ? q : (near ? p * (expm1f(r) - r) : t.G - p + q);
   } else {
@@ -79,6 +86,7 @@ __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
       lqm = -log1pf((1.f - beta) * expm1f(-r));
       lpm = lqm - r;
     }
+    t.F = (1.f - beta) * lpm;
     t.G = p == 0.f ? 0.f : (1.f - beta) * p * lpm;
     t.loss = (q == 0.f ? 0.f : beta * q * lqm) + t.G;
   }
@@ -119,23 +127,24 @@ __device__ __forceinline__ float exp_over_T(float d, const DistillParams& p) {
 }
 
 // What the teacher's list says (one warp): log q_k = lq_k - shift, the mass of the list and
-// outside it, sum q - 1, and (tail) the shift that renormalises it.
+// outside it, sum q - 1, and (tail) the list's mass once more.
 struct Teacher {
-  float shift, list, rest, over, log_list;
+  float shift, list, rest, over;
+  double sum;
 };
 __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) {
   const int lane = threadIdx.x & 31;
-  Teacher t{0.f, 1.f, 0.f, 0.f, 0.f};
+  Teacher t{0.f, 1.f, 0.f, 0.f, 1.0};
   if (tail) {
     double sum = 0.0;
     for (int k = lane; k < K; k += 32)
       if (sl.id[k] >= 0) sum += exp(static_cast<double>(sl.lq[k]));
     sum = warp_sum(sum);
     const double left = 1.0 - sum, rest = left < kRestMin ? kRestMin : left;  // a NaN stays one
+    t.sum = sum;
     t.list = static_cast<float>(sum);
     t.rest = static_cast<float>(rest);
     t.over = static_cast<float>(rest - left);
-    t.log_list = static_cast<float>(log(sum));
   } else {
     float m = -INFINITY;
     for (int k = lane; k < K; k += 32)
@@ -157,10 +166,26 @@ __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) 
   return t;
 }
 
+// The same renormalised over the list, for a row without a rest.
+__device__ __forceinline__ Teacher renormalised(double sum) {
+  int e;
+  const float m = static_cast<float>(frexp(sum, &e));  // a mass below fp32's range counts too
+  return Teacher{fmaf(static_cast<float>(e), kLn2, logf(m)), 1.f, 0.f, 0.f, 1.0};
+}
+
 // log(q / p) of the rest, d = q - p
 __device__ __forceinline__ float rest_ratio(float q, float p, float d) {
   const float e = d / p;
   return fabsf(e) < 0.5f ? log1pf(e) : logf(q / p);
+}
+// The same of a faint p = s e^a.
+__device__ __forceinline__ float faint_ratio(float q, float s, float a) { return logf(q / s) - a; }
+
+// G / p of the rest.  Below fp32's normal numbers G may be less than they hold; a factor past fp32
+// belongs to columns without any mass.
+__device__ __forceinline__ float rest_factor(const Term& t, float p) {
+  if (p >= FLT_MIN) return t.G / p;
+  return fabsf(t.F) <= FLT_MAX ? t.F : 0.f;
 }
 
 // The unlisted columns' gradient g F p_j as f 2^((x_j - x0) c), from p_j = 2^((x_j - x0) c) scale.
@@ -179,11 +204,24 @@ __device__ __forceinline__ Stream stream_of(float g, float F, float scale, float
   return Stream{g * (F * down * scale) * (down * (1.f + z.lo)), x1};
 }
 
+// The stream of a faint rest, whose columns have the statistic `rest`: at beta = 0 G_rest is -q (p S is
+// nothing beside it), and p_j / p_rest = 2^((x_j - m) c) / s.  Otherwise G / p and p_j are in range.
+__device__ __forceinline__ Stream faint_stream(const MaxStat& rest, float lse, float q, float S, float g,
+                                               const DistillParams& p) {
+  if (p.beta == 0.f && q > 0.f) return stream_of(g, -q, 1.f / rest.s, rest.m, p);
+  const Scaled z = over_T(rest.m, p);
+  const Term t = bucket(q, 0.f, faint_ratio(q, rest.s, (z.hi - lse) + z.lo), p.beta);
+  const float x0 = lse * p.T;
+  const Scaled z0 = over_T(x0, p);
+  return stream_of(g, rest_factor(t, 0.f) - S, expf((z0.hi - lse) + z0.lo), x0, p);
+}
+
 // One row's results (every lane of the list warp); the slots then hold G_k and p_k.
 struct RowResult {
   float loss, lse, p_rest;
-  float m, inv_s;   // p_j = 2^((x_j - m) c) inv_s
-  float S, F_rest;  // sum of G, G_rest / p_rest
+  float m, inv_s;  // p_j = 2^((x_j - m) c) inv_s
+  float S, F;      // sum of G, G_rest / p_rest
+  bool faint;
 };
 
 // The slots and the rest of a row, from the statistic `st` of the columns outside the list.
@@ -206,7 +244,7 @@ __device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const Te
     const float d = sl.x[k] - m;
     const Scaled z = over_T(d, p);
     const float pk = exp_over_T(d, p) * inv_s, lq = sl.lq[k] - te.shift;
-    const Term t = bucket(expf(lq), pk, pk == 0.f ? INFINITY : ((lq - z.hi) + ln_s) - z.lo, p.beta);
+    const Term t = bucket(expf(lq), pk, ((lq - z.hi) + ln_s) - z.lo, p.beta);
     loss += t.loss;
     S += t.G;
     sl.lq[k] = t.G;
@@ -214,8 +252,11 @@ __device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const Te
   }
   const float pr = s_rest * inv_s, pl = s_list * inv_s;
   const float dr = pr > 0.5f && te.over == 0.f ? pl - te.list : te.rest - pr;  // q_rest - p_rest
-  const Term t = bucket(te.rest, pr, rest_ratio(te.rest, pr, dr), p.beta);
   RowResult o;
+  o.faint = pr < FLT_MIN && st.s != 0.f;
+  const Scaled zr = over_T(st.m - m, p);
+  const float r = o.faint ? faint_ratio(te.rest, st.s * inv_s, zr.hi + zr.lo) : rest_ratio(te.rest, pr, dr);
+  const Term t = bucket(te.rest, pr, r, p.beta);
   const Scaled zm = over_T(m, p);
   o.lse = zm.hi + ln_s;
   // relative to the lse as it is stored: the backward's other p_j are too, and the common factor
@@ -226,7 +267,7 @@ __device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const Te
   o.m = m;
   o.inv_s = inv_s;
   o.S = warp_sum(S) + t.G;
-  o.F_rest = pr == 0.f ? 0.f : t.G / pr;
+  o.F = rest_factor(t, pr);
   return o;
 }
 
@@ -520,7 +561,7 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
     const MaxStat* stats = CS > 1 ? sh_parts : sh_stat;
     const MaxStat st = maxstat_warp(lane < kStats ? stats[lane] : MaxStat{-FLT_MAX, 0.f}, c);
     const float g = FUSED ? p.dloss[r] / p.T : 0.f;
-    if (p.tail && st.s == 0.f) te = Teacher{te.log_list, 1.f, 0.f, 0.f, 0.f};  // there is no rest
+    if (p.tail && st.s == 0.f) te = renormalised(te.sum);  // there is no rest
     const RowResult o = finish_row(sl, K, te, st, p);
     const float nan = __int_as_float(0x7FC00000);
     bad = __any_sync(0xFFFFFFFFu, bad);
@@ -532,7 +573,8 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
     if (FUSED) {
       for (int k = lane; k < K; k += 32) sl.lq[k] = bad ? nan : g * (sl.lq[k] - sl.x[k] * o.S);
       if (lane == 0) {
-        const Stream t = stream_of(g, o.F_rest - o.S, o.inv_s, o.m, p);
+        const Stream t =
+            o.faint ? faint_stream(st, o.lse, te.rest, o.S, g, p) : stream_of(g, o.F - o.S, o.inv_s, o.m, p);
         sh_factor = g == 0.f ? 0.f : (bad ? nan : t.f);
         sh_m = t.x0;
         sh_stat[0].s = g;
@@ -558,13 +600,66 @@ __global__ void __launch_bounds__(THREADS + 32, THREADS == 256 && !FUSED ? 5 : 0
       if (sl.id[k] >= 0) E::store_scalar(out + sl.id[k], sl.lq[k]);
 }
 
+// The statistic of a row's columns outside the list, whose slots are loaded (the backward of a faint
+// rest; all threads call).  Vectors with a listed column are found by a bit per vector, places shared
+// modulo kMarks; only those look through the list.  One vector in flight, so that the kernel's registers
+// do not grow for it (four in flight: 56 of them where the stream takes 32 to 40): such rows take twice
+// the time of others.
+constexpr int kMarks = 8192;
+template <class E, int THREADS>
+__device__ __forceinline__ MaxStat rest_stat(const typename E::storage* row, const Slots sl, int K, int V, float c) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ uint32_t marks[kMarks / 32];
+  __shared__ MaxStat sh[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int i = tid; i < kMarks / 32; i += THREADS + 32) marks[i] = 0u;
+  __syncthreads();
+  const RowSplit sp = split_row<E>(row, V);
+  if (tid >= THREADS)
+    for (int k = lane; k < K; k += 32) {
+      const int j = sl.id[k] - sp.head;
+      if (sl.id[k] < 0 || j < 0) continue;  // the head and the tail look through the list anyway
+      const unsigned v = static_cast<unsigned>(j / E::kVec) % kMarks;
+      atomicOr(&marks[v >> 5], 1u << (v & 31u));
+    }
+  __syncthreads();
+  if (tid < THREADS) {
+    MaxRun rs;
+    auto scalar = [&](int j) {
+      if (listed_bits(sl, K, j, 1) == 0u) maxrun_scalar(rs, E::load_scalar_coherent(row + j), c);
+    };
+    if (tid < sp.head) scalar(tid);
+    if (tid < sp.tail) scalar(sp.head + sp.nvec * E::kVec + tid);
+    const uint4* vb = reinterpret_cast<const uint4*>(row + sp.head);
+    for (int i = tid; i < sp.nvec; i += THREADS) {
+      uint4 v[1] = {ld_v4(vb + i)};
+      const unsigned q = static_cast<unsigned>(i) % kMarks;
+      if (marks[q >> 5] >> (q & 31u) & 1u)
+        drop(v[0], listed_bits(sl, K, sp.head + i * E::kVec, E::kVec), static_cast<E*>(nullptr));
+      maxrun_vectors<E>(rs, v, c);
+    }
+    const MaxStat st = maxstat_warp(rs.stat(), c);
+    if (lane == 0) sh[tid >> 5] = st;
+  }
+  __syncthreads();
+  return maxstat_warp(lane < kWarps ? sh[lane] : MaxStat{-FLT_MAX, 0.f}, c);
+}
+
+// CTAs of the backward per SM that its registers are held to: as many as the stream alone allows,
+// rest_stat aside (with its registers 8192 rows of 4 KB take 24.3 us, 21.1 us without; 2048 rows of 128 KB
+// of fp32 86 us and 78 us).
+template <class E, int THREADS, int UNROLL, bool SAME_PHASE>
+constexpr int kBwdPlaces =
+    UNROLL != kUnroll || !SAME_PHASE ? 0 : (THREADS == 64 ? 21 : (sizeof(typename E::storage) == 2 ? 5 : 7));
+
 // The backward: the list warp works out the row's factor and the listed columns' gradients, then
 // the others stream the row as rowgrad_kernel does.
 template <class E, int THREADS, int UNROLL, bool SAME_PHASE>
-__global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const DistillParams p, int parts) {
+__global__ void __launch_bounds__(THREADS + 32, kBwdPlaces<E, THREADS, UNROLL, SAME_PHASE>)
+    distill_bwd_kernel(const DistillParams p, int parts) {
   using S = typename E::storage;
   extern __shared__ uint4 distill_smem[];
-  __shared__ float sh_factor, sh_x0;
+  __shared__ float sh_factor, sh_x0, sh_faint, sh_S;
   wait_for_previous_grids();
   const int64_t r = blockIdx.x / static_cast<unsigned>(parts);
   const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
@@ -598,29 +693,37 @@ __global__ void __launch_bounds__(THREADS + 32) distill_bwd_kernel(const Distill
       const Scaled z = over_T(sl.x[k], p);
       const float lp = z.hi - lse, lq = sl.lq[k] - te.shift;  // lp: near lse, so the difference is exact
       const float pk = expf(lp + z.lo);
-      const Term t = bucket(expf(lq), pk, pk == 0.f ? INFINITY : (lq - lp) - z.lo, p.beta);
+      const Term t = bucket(expf(lq), pk, (lq - lp) - z.lo, p.beta);
       S_sum += t.G;
       sl.x[k] = pk;
       sl.lq[k] = t.G;
     }
+    // of a faint rest only G_rest, which is -q_rest at beta = 0 and next to nothing else; its stream below
+    const bool faint = p.tail && p_rest != 0.f && p_rest < FLT_MIN;
     const Term t = bucket(te.rest, p_rest, rest_ratio(te.rest, p_rest, te.rest - p_rest), p.beta);
-    S_sum = warp_sum(S_sum) + t.G;
+    S_sum = warp_sum(S_sum) + (!faint ? t.G : (p.beta == 0.f ? -te.rest : 0.f));
     for (int k = lane; k < K; k += 32) sl.lq[k] = g * (sl.lq[k] - sl.x[k] * S_sum);
     // p_j = 2^((x_j - x0) c) e^(x0 / T - lse): x0 takes up lse, so that no exponent is a small
     // difference of large products
     if (lane == 0) {
       const float x0 = lse * p.T;
       const Scaled z = over_T(x0, p);
-      const Stream st = stream_of(g, (p_rest == 0.f ? 0.f : t.G / p_rest) - S_sum, expf((z.hi - lse) + z.lo), x0, p);
+      const Stream st = stream_of(g, rest_factor(t, p_rest) - S_sum, expf((z.hi - lse) + z.lo), x0, p);
       sh_factor = st.f;
       sh_x0 = st.x0;
+      sh_faint = faint ? te.rest : 0.f;
+      sh_S = S_sum;
     }
   }
   __syncthreads();
+  Stream st{sh_factor, sh_x0};
+  if (sh_faint != 0.f) {
+    const MaxStat rest = rest_stat<E, THREADS>(row, sl, K, V, p.c);
+    st = faint_stream(rest, p.lse[r], sh_faint, sh_S, g, p);
+  }
   if (!list_warp) {
-    const float f = sh_factor;
-    if (f == 0.f) fill_span<E, THREADS>(out, sp, sn, 0u);
-    else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, sp, sn, sh_x0, p.c, f);
+    if (st.f == 0.f) fill_span<E, THREADS>(out, sp, sn, 0u);
+    else grad_stream<E, THREADS, UNROLL, SAME_PHASE>(row, out, sp, sn, st.x0, p.c, st.f);
   }
   __syncthreads();  // the listed columns' values go over the stream's
   if (list_warp)
