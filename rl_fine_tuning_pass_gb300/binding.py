@@ -468,13 +468,14 @@ def grpo_fused_linear(hidden, weight, idx, adv, dloss, *, B, L, T, beta, eps_low
 
 # A decode step calls these for microseconds of GPU work, so their marshalling is kept short:
 # descriptors are packed with ``struct`` (0.3 us; a ctypes structure takes 1.2 us), and the
-# stream and device are asked of torch's C layer (0.1 us each; torch.cuda's objects take 2 us).
+# stream and device are asked of torch's C layer (0.1 us each; torch.cuda's objects take 2 us),
+# where torch has one: a CPU build does not, and can still import this module.
 _ROWS = struct.Struct("=Qiiqqqqq")
 _RULES = struct.Struct("=QqqQQQQQQQqQqq")
 assert _ROWS.size == ctypes.sizeof(GrpoRows) and _RULES.size == ctypes.sizeof(GrpoLogitRules)
 _DTYPES = {torch.bfloat16: GRPO_BF16, torch.float32: GRPO_FP32}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_raw_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", lambda: torch.cuda.current_device())
 
 
 def _pack_rows(t: torch.Tensor):
