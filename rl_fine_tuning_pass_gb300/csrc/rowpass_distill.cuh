@@ -77,13 +77,14 @@ __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
     t.G = p == 0.f ? 0.f : -p * r;
     t.loss = p == 0.f ? q : (near ? p * (expm1f(r) - r) : t.G - p + q);
   } else {
-    // log(p/m) and log(q/m) from r alone: m/p = 1 + beta (e^r - 1), m/q = 1 + (1 - beta)(e^-r - 1)
+    // log(p/m) and log(q/m) from r alone: m/p = 1 + beta (e^r - 1), m/q = 1 + (1 - beta)(e^-r - 1), which
+    // for a small beta is beta + (1 - beta) e^-r (1 - beta has lost beta's digits)
     float lpm, lqm;
     if (r <= 0.f) {
       lpm = -log1pf(beta * expm1f(r));
       lqm = r + lpm;
     } else {
-      lqm = -log1pf((1.f - beta) * expm1f(-r));
+      lqm = beta < 0.25f && r > 0.5f ? -logf(fmaf(1.f - beta, expf(-r), beta)) : -log1pf((1.f - beta) * expm1f(-r));
       lpm = lqm - r;
     }
     t.F = (1.f - beta) * lpm;
