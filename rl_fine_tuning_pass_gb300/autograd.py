@@ -103,14 +103,14 @@ def entropy(logits, T=1.0):
 
 class ProcessLogitsFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, rules):
+    def forward(ctx, logits, rules, dev_err):
         # tensors are kept by the graph, not by the context, so that a change in place between
         # the passes is noticed; the logits are read again for the repetition penalty only
         ctx.names = [k for k, v in rules.items() if v is not None]
         ctx.keeps_logits = rules["repetition"] is not None
         ctx.save_for_backward(*([logits] if ctx.keeps_logits else []), *(rules[k] for k in ctx.names))
-        ctx.dtype = logits.dtype
-        return rp.process_logits_fwd(logits, **rules)
+        ctx.dtype, ctx.dev_err = logits.dtype, dev_err
+        return rp.process_logits_fwd(logits, **rules, dev_err=dev_err)
 
     @staticmethod
     @once_differentiable
@@ -120,22 +120,23 @@ class ProcessLogitsFunction(torch.autograd.Function):
         if dout.dtype != ctx.dtype or dout.stride(-1) != 1:
             dout = dout.to(ctx.dtype).contiguous()
         logits = kept.pop(0) if ctx.keeps_logits else dout
-        return rp.process_logits_bwd(logits, dout, **dict(zip(ctx.names, kept))), None
+        return rp.process_logits_bwd(logits, dout, **dict(zip(ctx.names, kept)), dev_err=ctx.dev_err), None, None
 
 
 def process_logits(logits, *, tokens=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
-                   presence=None, bias_ids=None, bias=None, allowed=None):
+                   presence=None, bias_ids=None, bias=None, allowed=None, dev_err=None):
     """The logits under the sampler's rules (see process_logits_fwd), differentiable with
-    respect to ``logits``; penalties, biases and masks are constants."""
+    respect to ``logits``; penalties, biases and masks are constants.  ``dev_err``: int32 word on
+    the GPU into which both passes OR their error bits."""
     return ProcessLogitsFunction.apply(logits, dict(
         tokens=tokens, hist_len=hist_len, prompt_len=prompt_len, repetition=repetition, frequency=frequency,
-        presence=presence, bias_ids=bias_ids, bias=bias, allowed=allowed))
+        presence=presence, bias_ids=bias_ids, bias=bias, allowed=allowed), dev_err)
 
 
 class DistillTopkFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, ids, teacher_logp, mask, T, beta, tail):
-        out = rp.distill_topk_fwd(logits, ids, teacher_logp, T=T, beta=beta, tail=tail, mask=mask)
+    def forward(ctx, logits, ids, teacher_logp, mask, T, beta, tail, dev_err):
+        out = rp.distill_topk_fwd(logits, ids, teacher_logp, T=T, beta=beta, tail=tail, mask=mask, dev_err=dev_err)
         ctx.save_for_backward(logits, ids, teacher_logp, out["lse"], out["p_rest"],
                               *(() if mask is None else (mask,)))
         ctx.scalars = (T, beta, tail)
@@ -149,11 +150,12 @@ class DistillTopkFunction(torch.autograd.Function):
         T, beta, tail = ctx.scalars
         dl = rp.distill_topk_bwd(logits, ids, tlogp, dloss.float().contiguous(), lse, p_rest, T=T, beta=beta, tail=tail,
                                  mask=mask[0] if mask else None)
-        return dl, None, None, None, None, None, None
+        return dl, None, None, None, None, None, None, None
 
 
-def distill_topk_loss(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, mask=None):
+def distill_topk_loss(logits, ids, teacher_logp, *, T=1.0, beta=0.0, tail=False, mask=None, dev_err=None):
     """Per-row divergence [B*L] from a teacher's top log-probs (see distill_topk_fwd) and the
     student's mass outside the list [B*L].  The loss is differentiable with respect to
-    ``logits``; the teacher is a constant."""
-    return DistillTopkFunction.apply(logits, ids, teacher_logp, mask, T, beta, tail)
+    ``logits``; the teacher is a constant.  ``dev_err``: int32 word on the GPU into which the
+    forward ORs its error bits (a NaN row's reason)."""
+    return DistillTopkFunction.apply(logits, ids, teacher_logp, mask, T, beta, tail, dev_err)
