@@ -609,8 +609,8 @@ def topk_log_softmax(logits, K, *, T=1.0):
     fp32), by falling logit, ties by rising column.  1 <= K <= min(V, 256)."""
     x, B, L, _ = _pack_rows(logits)
     dev = logits.device
-    R, K = B * L, int(K)
-    n = max(K, 0)
+    R, K = B * L, max(-1, min(int(K), 1 << 30))   # what the C side refuses stays refused in its 64 bits
+    n = max(0, min(K, GRPO_TOPK_MAX))
     ids = torch.empty((R, n), dtype=torch.int64, device=dev)
     logp = torch.empty((R, n), dtype=torch.float32, device=dev)
     lse = torch.empty(R, dtype=torch.float32, device=dev)
