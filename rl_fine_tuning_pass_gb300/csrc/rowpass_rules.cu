@@ -604,8 +604,9 @@ cudaError_t launch_e(const RulesParams& p, int64_t rows, int sms, cudaStream_t s
       return launch_bulk<E, BWD, false, many>(p, grid, tiles, run, runs, words, s);
     if constexpr (BWD) return launch_bulk<E, BWD, true, many>(p, grid, tiles, run, runs, words, s);
   }
-  return launch_after_previous_smem(rules_kernel<E, BWD, HOW>, grid, block, words, s, p, tiles, static_cast<int>(run),
-                                    static_cast<int>(runs));
+  if constexpr (!(BWD && HOW == kInPhase))  // which the bulk kernel takes whole
+    return launch_after_previous_smem(rules_kernel<E, BWD, HOW>, grid, block, words, s, p, tiles, static_cast<int>(run),
+                                      static_cast<int>(runs));
 }
 
 template <class E, bool BWD>
