@@ -768,7 +768,7 @@ int row_parts(const DistillParams& p, int64_t rows, int64_t places) {
 }
 
 // Streaming threads of the forward, and vectors in flight of each: 64 x 4 for short rows; 128 x 8 while
-// that leaves most rows resident (7 such CTAs per SM: 2048 rows of 64 KB 26 us, against 30 us with
+// that leaves most rows resident (6 such CTAs per SM: 2048 rows of 64 KB 26 us, against 30 us with
 // 256 x 4 and 34 us with 256 x 8, whose last step is mostly empty), in clusters while rows leave SMs
 // idle; else 256 x 4.
 template <class E>

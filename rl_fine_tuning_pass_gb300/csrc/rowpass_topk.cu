@@ -486,12 +486,14 @@ __global__ void __launch_bounds__(kTopkThreads, 5) topk_kernel(const TopkParams 
   }
 }
 
-// CTAs per row: as many as keep all CTAs resident at once (4 of 256 threads per SM), each with
-// a step of the sweep (1024 vectors) or more.
+// CTAs per row: as many as keep four CTAs or fewer per SM (five fit), each with a step of the sweep
+// (1024 vectors) or more.  With parts of half a step the merge costs more than the sweep saves (64 rows
+// of 32000 fp32 at K = 64: 8.7 us, 15.2 us with twice the CTAs; one row of 8192 bf16 at K = 20: 4.6 and
+// 6.1 us; one of 32000: 6.6 and 6.4 us).
 template <class E>
 int pick_split(const TopkParams& p, int64_t rows, int sms) {
   int cs = 1;
-  while (cs < 8 && rows * cs * 2 <= 4LL * sms && p.x.V / E::kVec >= 1024 * cs) cs *= 2;
+  while (cs < 8 && rows * cs * 2 <= 4LL * sms && p.x.V / E::kVec >= 2048 * cs) cs *= 2;
   return cs;
 }
 
