@@ -78,8 +78,9 @@ typedef enum { GRPO_FP32 = 0, GRPO_BF16 = 1 } grpo_dtype;
 #define GRPO_DEVERR_IDX_OUT_OF_RANGE 1
 /* A kernel gave up waiting for its own asynchronous copies (about 2 s): a tensor-core GEMM of
  * grpo_fused_linear(_noalloc) (copies or MMAs), a row of grpo_loss_fused or distill_topk_fused
- * (the bulk copy of the part of the row kept in shared memory), or a row of process_logits_*.  Those outputs are not valid.  The kernel
- * returns without trapping (the GEMM with its TMEM freed). */
+ * (the bulk copy of the part of the row kept in shared memory), or a row of process_logits_*.
+ * Those outputs are not valid.  The kernel returns without trapping (the GEMM with its TMEM
+ * freed). */
 #define GRPO_DEVERR_TIMEOUT 2
 /* A row's list of teacher ids holds a column twice (distill_topk_*). */
 #define GRPO_DEVERR_DUPLICATE_ID 4
@@ -486,7 +487,8 @@ typedef struct {
   int64_t tokens_stride;     /* elements between sequences, >= 0 (0: one history for all) */
   int64_t N;                 /* 0 <= N < 2^19 */
   const int32_t* hist_len;   /* [B*L] row r's history is its sequence's first hist_len[r] tokens;
-                                NULL = N.  Taken into [0, N]; outside sets the error bit */
+                                NULL = N.  Taken into [0, N]; outside sets the error bit (where
+                                the call has tokens and a penalty to count them for) */
   const int32_t* prompt_len; /* [B] the first tokens are the prompt's: they count for repetition
                                 only; NULL = 0 */
   const float* repetition;   /* [B] > 0, or NULL (no such penalty) */

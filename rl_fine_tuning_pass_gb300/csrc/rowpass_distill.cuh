@@ -19,8 +19,8 @@
 // gradient at beta = 0, -g q_rest p_j / p_rest, from 2^((x_j - m_rest) c) / s_rest.  The backward, which
 // has p_rest alone, sweeps such a row once more for that statistic (rest_stat).
 //
-// Bound by HBM: 8192 rows of 151936 bf16, a quarter of them masked, take 279 us forward (6.7 TB/s),
-// 662 us backward (6.6 TB/s, reads and writes), 818 us fused.
+// Bound by HBM: 8192 rows of 151936 bf16, a quarter of them masked, take 281 us forward (6.6 TB/s),
+// 667 us backward (6.5 TB/s, reads and writes), 835 us fused.
 //
 // A CTA takes a row.  Its last warp, the list warp, does not stream: it reads the list, marks the
 // bitmap, and works out what the teacher says (with 64-bit exponentials, the rest's mass being
@@ -420,7 +420,7 @@ __device__ __forceinline__ bool in_span(const RowSplit& sp, const Span& sn, int 
 // once its factor is known, from L2 or (long rows, 512 threads) from the part kept in shared
 // memory, as in fused_kernel.
 // The forward of many rows is held to the registers that let five CTAs share an SM (8192 rows of 304
-// KB: 279 us, 300 us with four).
+// KB: 280 us, 300 us with four).
 // CS > 1 (forward of few rows): a cluster of CTAs takes a row, a part each; the first one gets the
 // parts' statistics and finishes the row.
 template <class E, int THREADS, int UNROLL, bool FUSED, bool SAME_PHASE, int CS>

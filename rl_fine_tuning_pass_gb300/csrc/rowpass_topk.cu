@@ -13,7 +13,8 @@
 //
 // Measured: the top 64 of 8192 rows of 151936 bf16 take 394 us (6.3 TB/s, 93% of the copy rate; radix
 // selection alone took 4.2 ms); what is left are the barriers of the bound and of the
-// ranking, which five CTAs per SM do not hide whole.
+// ranking, which five CTAs per SM do not hide whole.  They do not shrink with the row: the top 32 of 8192
+// rows of 600 take 60 us, of 4000 63 us.
 //
 // Rows that collect more than the buffers hold (thousands of ties at the K-th value) are done
 // again by radix selection on order-preserving keys.
