@@ -77,16 +77,25 @@ __device__ __forceinline__ Term bucket(float q, float p, float r, float beta) {
     t.G = p == 0.f ? 0.f : -p * r;
     t.loss = p == 0.f ? q : (near ? p * (expm1f(r) - r) : t.G - p + q);
   } else {
-    // log(p/m) and log(q/m) from r alone: m/p = 1 + beta (e^r - 1), m/q = 1 + (1 - beta)(e^-r - 1), which
-    // for a small beta is beta + (1 - beta) e^-r (1 - beta has lost beta's digits)
-    float lpm, lqm;
-    if (r <= 0.f) {
-      lpm = -log1pf(beta * expm1f(r));
-      lqm = r + lpm;
+    // log(p/m) and log(q/m) from r alone.  With b the weight of the larger of p and q, and s = |r|:
+    // m / larger = 1 + (1 - b)(e^-s - 1), m / smaller = 1 + b (e^s - 1).  For a small b the first has lost
+    // b's digits (it is b + (1 - b) e^-s then), and the second gives a log(smaller / m) near 0 its own
+    const bool up = r > 0.f;  // q is the larger
+    const float s = fabsf(r), b = up ? beta : 1.f - beta, nb = up ? 1.f - beta : beta;
+    float large, small;
+    if (b >= 0.25f) {
+      large = -log1pf(nb * expm1f(-s));
+      small = large - s;
     } else {
-      lqm = beta < 0.25f && r > 0.5f ? -logf(fmaf(1.f - beta, expf(-r), beta)) : -log1pf((1.f - beta) * expm1f(-r));
-      lpm = lqm - r;
+      const float a = b * expm1f(s);
+      small = -log1pf(a);
+      large = s + small;
+      if (!(a < 1.f)) {
+        large = -logf(fmaf(nb, expf(-s), b));
+        small = large - s;
+      }
     }
+    const float lpm = up ? small : large, lqm = up ? large : small;
     t.F = (1.f - beta) * lpm;
     t.G = p == 0.f ? 0.f : (1.f - beta) * p * lpm;
     t.loss = (q == 0.f ? 0.f : beta * q * lqm) + t.G;
