@@ -136,15 +136,17 @@ __device__ __forceinline__ float exp_over_T(float d, const DistillParams& p) {
   return fmaf(e, z.lo, e);
 }
 
-// What the teacher's list says (one warp): log q_k = lq_k - shift, the mass of the list and
-// outside it, sum q - 1, and (tail) the list's mass once more.
+// What the teacher's list says (one warp): log q_k = (lq_k - base) - shift (one number for both would
+// round a far-shifted list's q_k alike, and their sum with them), the mass of the list and outside it,
+// sum q - 1, and (tail) the list's mass once more.
 struct Teacher {
-  float shift, list, rest, over;
+  float base, shift, list, rest, over;
   double sum;
+  __device__ __forceinline__ float log_q(float lq) const { return (lq - base) - shift; }
 };
 __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) {
   const int lane = threadIdx.x & 31;
-  Teacher t{0.f, 1.f, 0.f, 0.f, 1.0};
+  Teacher t{0.f, 0.f, 1.f, 0.f, 0.f, 1.0};
   if (tail) {
     double sum = 0.0;
     for (int k = lane; k < K; k += 32)
@@ -167,7 +169,8 @@ __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) 
         sum += expf(sl.lq[k] - m);
         used = 1;
       }
-    t.shift = m + logf(warp_sum(sum));
+    t.base = m;
+    t.shift = logf(warp_sum(sum));
     if (!__any_sync(0xFFFFFFFFu, used)) {  // nothing listed
       t.list = 0.f;
       t.over = -1.f;
@@ -176,11 +179,15 @@ __device__ __forceinline__ Teacher teacher_of(const Slots& sl, int K, int tail) 
   return t;
 }
 
-// The same renormalised over the list, for a row without a rest.
+// The same renormalised over the list, for a row without a rest.  A mass below fp32's range counts too:
+// log(m 2^e) with e log 2 as a product that is exact in fp32 (log 2 to twelve bits) and what that leaves.
 __device__ __forceinline__ Teacher renormalised(double sum) {
+  constexpr double kLn2D = 0.69314718055994530942;
+  constexpr float kHigh = static_cast<float>(static_cast<int>(kLn2D * 4096.0) / 4096.0);
+  constexpr float kLow = static_cast<float>(kLn2D - static_cast<double>(kHigh));
   int e;
-  const float m = static_cast<float>(frexp(sum, &e));  // a mass below fp32's range counts too
-  return Teacher{fmaf(static_cast<float>(e), kLn2, logf(m)), 1.f, 0.f, 0.f, 1.0};
+  const float m = static_cast<float>(frexp(sum, &e)), n = static_cast<float>(e);
+  return Teacher{n * kHigh, fmaf(n, kLow, logf(m)), 1.f, 0.f, 0.f, 1.0};
 }
 
 // log(q / p) of the rest, d = q - p
@@ -253,7 +260,7 @@ __device__ __forceinline__ RowResult finish_row(const Slots& sl, int K, const Te
     if (sl.id[k] < 0) continue;
     const float d = sl.x[k] - m;
     const Scaled z = over_T(d, p);
-    const float pk = exp_over_T(d, p) * inv_s, lq = sl.lq[k] - te.shift;
+    const float pk = exp_over_T(d, p) * inv_s, lq = te.log_q(sl.lq[k]);
     const Term t = bucket(expf(lq), pk, ((lq - z.hi) + ln_s) - z.lo, p.beta);
     loss += t.loss;
     S += t.G;
@@ -701,7 +708,7 @@ __global__ void __launch_bounds__(THREADS + 32, kBwdPlaces<E, THREADS, UNROLL, S
     for (int k = lane; k < K; k += 32) {
       if (sl.id[k] < 0) continue;
       const Scaled z = over_T(sl.x[k], p);
-      const float lp = z.hi - lse, lq = sl.lq[k] - te.shift;  // lp: near lse, so the difference is exact
+      const float lp = z.hi - lse, lq = te.log_q(sl.lq[k]);  // lp: near lse, so the difference is exact
       const float pk = expf(lp + z.lo);
       const Term t = bucket(expf(lq), pk, (lq - lp) - z.lo, p.beta);
       S_sum += t.G;

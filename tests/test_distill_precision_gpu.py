@@ -6,7 +6,7 @@ import torch
 from logits_ops_util import DEV, f64, randn
 from oracle import logits_ops_oracle as lo
 from rl_fine_tuning_pass_gb300 import binding as rp
-from test_distill_topk_gpu import EPS
+from test_distill_topk_gpu import EPS, check
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -57,3 +57,20 @@ def test_gradients_of_mixtures_relative_to_the_smaller_weight(beta, tail):
     for name, got in (("backward", dl), ("fused", u["dlogits"])):
         off = np.abs(f64(got) - o["dlogits"]) - tol
         assert off.max() <= 0, f"{name}: {int((off > 0).sum())} outside, worst {off.max() / min(b, 1 - b):.3g} of the weight"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("beta", [0.0, 0.5])
+@pytest.mark.parametrize("shift", [-300.0, -20.0, 60.0])
+def test_a_shifted_teacher_is_the_same(dtype, beta, shift):
+    """Without the tail the teacher is renormalised: a shift of its log-probs, as fp32 holds them,
+    changes nothing; also where a student's rest has no mass and the tail is asked for."""
+    V, K = 203, 30
+    x = (randn(1, 6, V, seed=4) * 12).to(dtype)
+    x[0, 4:] = float("-inf")
+    x[0, 4:, 50:50 + K] = (randn(2, K, seed=6) * 12).to(dtype)
+    ids = torch.arange(50, 50 + K).repeat(6, 1)
+    lp = torch.log_softmax(randn(6, K, seed=5), 1) + shift
+    check(x.to(DEV), ids, lp, 1.0, beta, False, what=f"shift {shift}")
+    if shift < 0:
+        check(x[:, 4:].to(DEV), ids[4:], lp[4:], 1.0, beta, True, what=f"no rest, shift {shift}")
