@@ -553,6 +553,9 @@ grpo_status topk_log_softmax(const grpo_rows* logits, int64_t K, float T, int64_
  *   dlogits_rj = (dloss_r / T) (G_k - p_j S) at a listed column,
  *                (dloss_r / T) p_j (G_rest / p_rest - S) at the others
  *
+ * The terms' log-ratios are those of the logits and stay finite however little a mass is; the
+ * masses that weigh them are fp32: one below 2^-149 is 0, and 0 log 0 = 0.
+ *
  *   logits        [B, L, V];  T > 0 finite;  0 <= beta <= 1
  *   ids           [B*L][K] int64 listed columns, all different; a negative id is an unused
  *                 slot.  1 <= K <= GRPO_DISTILL_MAX_K
