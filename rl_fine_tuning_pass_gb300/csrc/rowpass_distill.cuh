@@ -831,8 +831,8 @@ cudaError_t launch_distill_fused_t(bool same_phase, const DistillParams& p, int6
 
 // The part of long rows that is kept is that of grpo_loss_fused less the bitmap and the list, so that
 // two CTAs still share an SM.  Shorter rows: 128 streaming threads, eight vectors in flight each (2048
-// rows of 64 KB: 51 us; 58 us with four in flight, 61 us with 256 x 4: more CTAs are in different phases
-// of their rows).
+// rows of 64 KB, on one machine: 51 us; 58 us with four in flight, 61 us with 256 x 4: more CTAs are in
+// different phases of their rows; others take up to 66 us).
 template <class E>
 cudaError_t launch_distill_fused_e(bool same_phase, const DistillParams& p, int64_t rows, int sms, cudaStream_t s) {
   (void)sms;
