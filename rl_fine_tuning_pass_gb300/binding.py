@@ -791,7 +791,7 @@ def preference_loss_fused(logits, idx, dloss, *, T=1.0, beta=0.1, kind="sigmoid"
 
 
 _ptrs_of, _numels_of, _devices_of = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
-_dtype_of, _bytes_of = attrgetter("dtype"), attrgetter("nbytes")
+_dtype_of = attrgetter("dtype")
 _contiguous, _NONE = torch.Tensor.is_contiguous, type(None)
 
 

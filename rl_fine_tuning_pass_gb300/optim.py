@@ -109,7 +109,7 @@ class AdamW:
                 self.scale.data_ptr() + 8 * f if self.scale is not None else 0, n, rp._DTYPES[p.dtype], word])
         self._table, self._counts = table, table[6::_WORDS]
         self._param_words = table[7::_WORDS]
-        self._shapes, self._bytes = [p.shape for p in self.params], list(map(rp._bytes_of, self.params))
+        self._shapes, self._dtypes = [p.shape for p in self.params], list(map(rp._dtype_of, self.params))
         self._grad_dtypes = None                                  # of the last call, and their words
 
     def views(self, flat):
@@ -168,9 +168,10 @@ class AdamW:
         grads = [p.grad for p in params] if grads is None else list(grads)
         if len(grads) != len(params):
             raise ValueError(f"{len(params)} gradients are needed, got {len(grads)}")
-        # a parameter's memory was exchanged, or is seen in another size, order or type
-        if list(map(rp._ptrs_of, params)) != self._pointers or list(map(rp._bytes_of, params)) != self._bytes or \
-                not all(map(rp._contiguous, params)):
+        # a parameter's memory was exchanged, or is seen in another type, size or order (in any of them alone:
+        # another type over the same bytes is another size)
+        if list(map(rp._ptrs_of, params)) != self._pointers or list(map(rp._dtype_of, params)) != self._dtypes or \
+                list(map(rp._numels_of, params)) != self.numels or not all(map(rp._contiguous, params)):
             self._check_params()
             if list(map(rp._numels_of, params)) != self.numels:
                 raise ValueError("a parameter has another size than at the start")
