@@ -29,7 +29,8 @@ class AdamW:
                   step follows it); may be set between steps
     weight_decay  one value, or one for each tensor
     state_bits    32, or 8: moments in 8-bit codes, 256 of a tensor's elements to a pair of scales
-    master        keep an fp32 copy of bf16 parameters, which are then its rounding
+    master        keep an fp32 copy of bf16 parameters, which are then its rounding (one that becomes bf16
+                  later has it from its next step on)
     stochastic    round what is kept in few bits (the second moment's codes, bf16 parameters without
                   a master copy) up or down by random bits, so that changes below its precision
                   are kept on average.  Default: with 8-bit states
@@ -70,7 +71,7 @@ class AdamW:
         kind = dict(dtype=torch.uint8 if state_bits == 8 else torch.float32, device=dev)
         self.exp_avg, self.exp_avg_sq = torch.zeros(total, **kind), torch.zeros(total, **kind)
         self.scale = torch.zeros(at, 2, dtype=torch.float32, device=dev) if state_bits == 8 else None
-        self.master = None
+        self.master, self._masters = None, bool(master)
         if master and any(p.dtype == torch.bfloat16 for p in self.params):
             self.master = torch.zeros(total, dtype=torch.float32, device=dev)
             self.reset_master()
@@ -120,6 +121,21 @@ class AdamW:
         """Take the master copies from the parameters (after these were loaded)."""
         for p, v in zip(self.params, self.views(self.master)):
             v.copy_(p.detach())
+
+    def _follow_types(self):
+        """A parameter that has become bf16 since the table was built takes its master copy from itself: what
+        its slot holds is of the start, or of the last time that it was bf16."""
+        became = [i for i, (p, was) in enumerate(zip(self.params, self._dtypes))
+                  if p.dtype == torch.bfloat16 and was != torch.bfloat16]
+        if not became or not self._masters:
+            return
+        if torch.cuda.is_current_stream_capturing():   # the copy would be repeated by each replay
+            raise RuntimeError("a parameter has become bf16: make a step before the capture")
+        if self.master is None:
+            self.master = torch.zeros(self.exp_avg.numel(), dtype=torch.float32, device=self.device)
+        views = self.views(self.master)
+        for i in became:
+            views[i].copy_(self.params[i].detach())
 
     def moments(self):
         """(exp_avg, exp_avg_sq) as fp32 in the flat layout: the states themselves with 32 bits, what
@@ -175,6 +191,7 @@ class AdamW:
             self._check_params()
             if list(map(rp._numels_of, params)) != self.numels:
                 raise ValueError("a parameter has another size than at the start")
+            self._follow_types()
             self._build()
         table, counts, shapes = self._table[:], self._counts, self._shapes
         missing, given = (), grads

@@ -27,6 +27,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(rp, "_call", note)
     monkeypatch.setattr(rp, "grad_dtypes", lambda grads, dev: [g.dtype for g in grads])
     monkeypatch.setattr(AdamW, "_check_params", lambda self: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return seen
 
 
@@ -65,3 +66,47 @@ def test_as_many_elements_of_another_type_are_followed(calls):
     first, second = calls[0][0], calls[1][0]
     assert first.param == second.param and first.n == second.n == 32
     assert first.types == (rp.GRPO_FP32, rp.GRPO_FP32) and second.types == (rp.GRPO_BF16, rp.GRPO_FP32)
+
+
+def test_a_parameter_that_becomes_bf16_takes_its_master_copy_anew(calls):
+    """Not what its slot was filled with at the start, or left with when it was bf16 before."""
+    memory = torch.full((32,), 3.0)
+    p, q = torch.nn.Parameter(memory), torch.nn.Parameter(torch.ones(32, dtype=BF16))
+    opt = AdamW([p, q], master=True)
+    g = [torch.zeros(32), torch.zeros(32)]
+    opt.step(g)
+    assert calls[-1][0].master is None and calls[-1][1].master == opt.views(opt.master)[1].data_ptr()
+    for value in (5.0, 7.0):
+        opt.views(opt.master)[1].fill_(value + 0.001)           # the other's copy is the update's
+        p.data = memory.view(BF16)[:32].fill_(value)
+        opt.step(g)
+        assert calls[-1][0].master == opt.views(opt.master)[0].data_ptr()
+        assert bool((opt.views(opt.master)[0] == value).all())
+        assert bool((opt.views(opt.master)[1] == value + 0.001).all())
+        p.data = memory
+        opt.step(g)
+        assert calls[-1][0].master is None
+
+
+def test_the_first_parameter_that_becomes_bf16_gets_a_master_copy(calls):
+    memory = torch.zeros(300)
+    p = torch.nn.Parameter(memory)
+    opt = AdamW([p], master=True)
+    assert opt.master is None
+    p.data = memory.view(BF16)[:300].fill_(2.0)
+    opt.step([torch.zeros(300)])
+    assert calls[-1][0].master == opt.master.data_ptr() and bool((opt.views(opt.master)[0] == 2).all())
+    other = AdamW([p])                                          # without
+    other.step([torch.zeros(300)])
+    assert other.master is None and calls[-1][0].master is None
+
+
+def test_another_type_is_refused_while_a_graph_is_captured(calls, monkeypatch):
+    memory = torch.zeros(32)
+    p = torch.nn.Parameter(memory)
+    opt = AdamW([p], master=True)
+    p.data = memory.view(BF16)[:32]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="before the capture"):
+        opt.step([torch.zeros(32)])
+    assert not calls
