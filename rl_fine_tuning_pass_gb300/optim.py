@@ -113,6 +113,13 @@ class AdamW:
         self._shapes, self._dtypes = [p.shape for p in self.params], list(map(rp._dtype_of, self.params))
         self._grad_dtypes = None                                  # of the last call, and their words
 
+    def __setstate__(self, attributes):
+        """Of a copy, or of one that was saved: the table's addresses are the original's."""
+        self.__dict__.update(attributes)
+        self.device = self.params[0].device
+        self._check_params()
+        self._build()
+
     def views(self, flat):
         """Each tensor's part of a flat buffer, in its shape."""
         return [flat[f * BLOCK:f * BLOCK + n].view(p.shape) for p, n, f in zip(self.params, self.numels, self._first)]

@@ -1,6 +1,8 @@
 """AdamW's table follows what a parameter is now, on the CPU: the C call is replaced by one that notes the table
 it would have been given, and the checks that ask for CUDA tensors are left out."""
+import copy
 import ctypes
+import pickle
 from types import SimpleNamespace
 
 import pytest
@@ -22,7 +24,8 @@ def calls(monkeypatch):
         assert name == "adamw_step"
         rows = (rp.GrpoAdamwTensor * count).from_buffer_copy(
             ctypes.string_at(table, count * ctypes.sizeof(rp.GrpoAdamwTensor)))
-        seen.append([SimpleNamespace(param=t.param, n=t.n, types=(t.param_dtype, t.grad_dtype), master=t.master)
+        seen.append([SimpleNamespace(param=t.param, n=t.n, types=(t.param_dtype, t.grad_dtype), master=t.master,
+                                     states=(t.exp_avg, t.exp_avg_sq, t.scale))
                      for t in rows])
     monkeypatch.setattr(rp, "_call", note)
     monkeypatch.setattr(rp, "grad_dtypes", lambda grads, dev: [g.dtype for g in grads])
@@ -110,3 +113,16 @@ def test_another_type_is_refused_while_a_graph_is_captured(calls, monkeypatch):
     with pytest.raises(RuntimeError, match="before the capture"):
         opt.step([torch.zeros(32)])
     assert not calls
+
+
+@pytest.mark.parametrize("way", [copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o))])
+def test_a_copy_has_states_of_its_own(calls, way):
+    """Also where a parameter lies at the address that the original's had, as in a program that loads a saved one."""
+    p = torch.nn.Parameter(torch.zeros(300))
+    opt = AdamW([p], state_bits=8)
+    other = way(opt)
+    other.params[0].data = p.data
+    other.step([torch.zeros(300)])
+    assert calls[-1][0].param == p.data_ptr()
+    assert calls[-1][0].states == tuple(t.data_ptr() for t in (other.exp_avg, other.exp_avg_sq, other.scale))
+    assert other.exp_avg.data_ptr() != opt.exp_avg.data_ptr()
