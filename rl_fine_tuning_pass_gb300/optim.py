@@ -125,7 +125,9 @@ class AdamW:
         return [flat[f * BLOCK:f * BLOCK + n].view(p.shape) for p, n, f in zip(self.params, self.numels, self._first)]
 
     def reset_master(self):
-        """Take the master copies from the parameters (after these were loaded)."""
+        """Take the master copies, if there are any, from the parameters (after these were loaded)."""
+        if self.master is None:
+            return
         for p, v in zip(self.params, self.views(self.master)):
             v.copy_(p.detach())
 

@@ -126,3 +126,12 @@ def test_a_copy_has_states_of_its_own(calls, way):
     assert calls[-1][0].param == p.data_ptr()
     assert calls[-1][0].states == tuple(t.data_ptr() for t in (other.exp_avg, other.exp_avg_sq, other.scale))
     assert other.exp_avg.data_ptr() != opt.exp_avg.data_ptr()
+
+
+def test_without_master_copies_there_is_none_to_reset(calls):
+    p = torch.nn.Parameter(torch.ones(30, dtype=BF16))
+    AdamW([p]).reset_master()
+    opt = AdamW([p, torch.nn.Parameter(torch.ones(30))], master=True)
+    p.data.fill_(4.0)
+    opt.reset_master()
+    assert bool((opt.views(opt.master)[0] == 4).all())
