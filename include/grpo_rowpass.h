@@ -625,6 +625,7 @@ typedef struct {
  *                 margin is a small difference of sums of thousands of them)
  *   lse           [2P*L] fp32 output; logp and lse are +0.0 on masked rows, whose logits are not read
  *   dloss         [P] fp32 upstream gradient of each pair's loss
+ *   T             of the backward: as in the forward's args
  *   dlogits       as in grpo_loss_bwd (may alias logits exactly).  Rows with a zero factor (masked
  *                 ones; a hinge without loss; dloss == 0) are written as +0.0 and not read
  * An unmasked row whose idx is outside [0, V) sets GRPO_DEVERR_IDX_OUT_OF_RANGE; its logp, its
@@ -636,7 +637,7 @@ grpo_status preference_loss_fwd(const grpo_rows* logits, const int64_t* idx, con
                                 float* seq_logp, float* coef, float* logp, float* lse, int32_t* dev_err,
                                 grpo_stream_t stream);
 grpo_status preference_loss_bwd(const grpo_rows* logits, const int64_t* idx, const uint8_t* mask, const float* dloss,
-                                const float* coef, const float* lse, float T, const grpo_rows* dlogits,
+                                const float* coef, const float* lse, double T, const grpo_rows* dlogits,
                                 int32_t* dev_err, grpo_stream_t stream);
 grpo_status preference_loss_fused(const grpo_rows* logits, const int64_t* idx, const float* ref_logp,
                                   const uint8_t* mask, const float* dloss, const grpo_pref_args* args,

@@ -138,7 +138,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "distill_topk_bwd": [_P, _P, _P, ctypes.c_int64, _P, _P, _P, _P, _F, _F, ctypes.c_int32, _P, _P],
         "distill_topk_fused": [_P, _P, _P, ctypes.c_int64, _P, _P, _F, _F, ctypes.c_int32, _P, _P, _P, _P, _P, _P],
         "preference_loss_fwd": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
-        "preference_loss_bwd": [_P, _P, _P, _P, _P, _P, _F, _P, _P, _P],
+        "preference_loss_bwd": [_P, _P, _P, _P, _P, _P, ctypes.c_double, _P, _P, _P],
         "preference_loss_fused": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
         "grad_norm": [_P, ctypes.c_int64, _P, _P, ctypes.c_uint64, _P],
         "adamw_step": [_P, ctypes.c_int64, _P, _P, _P],

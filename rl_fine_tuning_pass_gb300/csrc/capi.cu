@@ -943,11 +943,11 @@ grpo_status preference_loss_fwd(const grpo_rows* logits, const int64_t* idx, con
 }
 
 grpo_status preference_loss_bwd(const grpo_rows* logits, const int64_t* idx, const uint8_t* mask, const float* dloss,
-                                const float* coef, const float* lse, float T, const grpo_rows* dlogits,
+                                const float* coef, const float* lse, double T, const grpo_rows* dlogits,
                                 int32_t* dev_err, grpo_stream_t stream) {
   grpo_status st = check_rows(logits);
   if (st != GRPO_OK) return st;
-  if (!finite_pos(T) || logits->B % 2 != 0) return GRPO_ERR_INVALID_ARG;
+  if (!finite_pos(static_cast<float>(T)) || logits->B % 2 != 0) return GRPO_ERR_INVALID_ARG;
   bool same_phase = false;
   if ((st = check_dlogits(logits, dlogits, &same_phase)) != GRPO_OK) return st;
   if (rows_of(logits) == 0) return GRPO_OK;
