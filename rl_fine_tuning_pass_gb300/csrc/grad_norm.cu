@@ -3,11 +3,14 @@
 // Squares are summed in two fp32 numbers: the sum, and what its roundings lost (a 64-bit addition takes
 // a warp some 300 cycles here, and those alone were half of the time).  Without the second number a
 // norm of bf16 gradients came out 6e-9 too small: half-way cases are common among sums of 16-bit
-// squares, and most are rounded down, for the square of an odd number is 1 modulo 8.  It takes one
-// addition as exact that is so only where the sum is not below the square, as it is after the
-// first few of the sixteen; what is left is below 1e-10.  An fp32 sum outside [2^-90, 2^80] may have lost what overflowed or fell below 2^-149, or
-// bring the total out of range: it is formed again from the elements, read once more and scaled by a
-// power of two, and goes into a 64-bit sum beside.  So the norm is right for every finite input.
+// squares, and most are rounded down, for the square of an odd number is 1 modulo 8.  What s = was + g^2 loses is
+// g^2 - (s - was), both exact as long as was is not below g^2; so a thread's sums start from a power of two above
+// all of its squares, which is taken off at the end.  (From 0, a spike behind small elements left norms 5e-8 off.)
+// What is left is the rounding of the losses' sum: up to k 2^-48 of the start at the k-th of a thread's sixteen
+// pairs, 2^-40 in all; the start is at most 64 of the largest square, so it is below 7e-11 of a sum.  600M bf16: 187 us, 183 without the start, 195 with sums of two
+// numbers that are exact in either order.  An fp32 sum outside [2^-90, 2^80] may have lost what overflowed or fell
+// below 2^-149, or bring the total out of range: it is formed again from the elements, read once more and scaled
+// by a power of two, and goes into a 64-bit sum beside.  So the norm is right for every finite input.
 // Partial sums are per CTA and added in a fixed order.
 #include <algorithm>
 #include <cmath>
@@ -61,6 +64,32 @@ __device__ __forceinline__ void load_share(Share<E>& x, const void* grad, int64_
   }
 }
 
+__device__ __forceinline__ float top_of(const Share<BF16>& x) {
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x.v[0].x));
+#pragma unroll
+  for (int k = 0; k < Share<BF16>::kVecs; ++k) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x.v[k]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(h[i]));
+  }
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float top_of(const Share<F32>& x) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < Share<F32>::kVecs; ++k)
+    m = fmaxf(fmaxf(fmaxf(m, fabsf(__uint_as_float(x.v[k].x))), fabsf(__uint_as_float(x.v[k].y))),
+              fmaxf(fabsf(__uint_as_float(x.v[k].z)), fabsf(__uint_as_float(x.v[k].w))));
+  return m;
+}
+// What a thread's sums start from: 2^(2e + 6), above all of their sixteen squares together, for a largest element
+// in [2^e, 2^(e + 1)).  (Held to fp32's exponents; the sum is out of [2^-90, 2^80] then.)
+template <class E>
+__device__ __forceinline__ float start_of(const Share<E>& x) {
+  const int e = 2 * static_cast<int>(__float_as_uint(top_of(x)) >> 23) - 121;
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 253)) << 23);
+}
+
 // The sum where its squares leave fp32's range: the thread's elements are read once more, and scaled by
 // 2^-e, e the largest one's exponent (as two factors, for 2^128 is not an fp32 number).
 template <class E>
@@ -99,7 +128,8 @@ __device__ __forceinline__ void add_chunk(Total& acc, const NormTensor& t, int64
   Share<E> x;
   load_share<E>(x, t.grad, base, n);
   const float2 minus = make_float2(-1.f, -1.f);
-  float2 s = make_float2(0.f, 0.f), lost = s;
+  const float start = start_of(x);
+  float2 s = make_float2(start, start), lost = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < Share<E>::kVecs; ++k)
 #pragma unroll
@@ -108,6 +138,7 @@ __device__ __forceinline__ void add_chunk(Total& acc, const NormTensor& t, int64
       s = __ffma2_rn(g, g, was);
       lost = __fadd2_rn(lost, __ffma2_rn(g, g, __ffma2_rn(s, minus, was)));
     }
+  s = __fadd2_rn(s, make_float2(-start, -start));  // exact
   const float sum = s.x + s.y;
   if (sum >= 0x1p-90f && sum <= 0x1p80f) {
     acc.near = two_add(two_add(acc.near, TwoSum{s.x, lost.x}), TwoSum{s.y, lost.y});
