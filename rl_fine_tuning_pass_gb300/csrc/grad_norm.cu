@@ -91,7 +91,8 @@ __device__ __forceinline__ float start_of(const Share<E>& x) {
 }
 
 // The sum where its squares leave fp32's range: the thread's elements are read once more, and scaled by
-// 2^-e, e the largest one's exponent (as two factors, for 2^128 is not an fp32 number).
+// 2^-e, e the largest one's exponent (as two factors, for 2^128 is not an fp32 number).  What
+// roundings lose is kept here too, from a start above all 32 squares: in error by 2^-32 at most.
 template <class E>
 __device__ __noinline__ double sum_scaled(const void* grad, int64_t base, int64_t n) {
   using S = typename E::storage;
@@ -110,12 +111,13 @@ __device__ __noinline__ double sum_scaled(const void* grad, int64_t base, int64_
   const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // -127 where top is subnormal
   const int half = e / 2;
   const float by = exp2f(static_cast<float>(-half)), again = exp2f(static_cast<float>(half - e));
-  float s = 0.f;
+  float s = 128.f, lost = 0.f;  // above 32 squares below 4
   for (int k = 0; k < kNormPer; ++k) {
-    const float g = element(k) * by * again;
-    s = fmaf(g, g, s);
+    const float g = element(k) * by * again, was = s;
+    s = fmaf(g, g, was);
+    lost += fmaf(g, g, was - s);
   }
-  return static_cast<double>(s) * exp2(2.0 * e);
+  return (static_cast<double>(s - 128.f) + static_cast<double>(lost)) * exp2(2.0 * e);
 }
 
 struct Total {

@@ -1,9 +1,10 @@
 """grad_norm where what a rounding of the sum loses is not to be had from one subtraction: a spike after small
-elements.
+elements, and sums outside fp32's range.
 
 A thread's sum is within 7e-11 of the squares' (the sum of what its roundings lose is itself rounded, up to k 2^-48 of
 at most 64 of the largest square at the k-th of sixteen pairs), what adds the threads' sums below 1e-12, and
-the norm within half of that.  So a norm that is 3e-10 from the middle of two fp32 numbers goes to the nearer one.
+the norm within half of that; sums out of range are within 2^-32 (32 squares, one by one).  So a norm that is 3e-10 from
+the middle of two fp32 numbers goes to the nearer one.
 """
 import numpy as np
 import pytest
@@ -72,3 +73,11 @@ def test_spikes_after_small_elements(n, side, dtype):
 def test_elements_in_any_order(side, dtype):
     for seed in range(6):
         check(numbers(np.random.default_rng(seed), 1 << 18, -11, -2), side, dtype)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 60, 2.0 ** -60, 2.0 ** 90, 2.0 ** -100])
+@pytest.mark.parametrize("side", [1, -1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sums_outside_the_range(scale, side, dtype):
+    for seed in range(6):
+        check(numbers(np.random.default_rng(seed), 1 << 18, -11, -2), side, dtype, scale)
