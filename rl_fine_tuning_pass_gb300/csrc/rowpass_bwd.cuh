@@ -96,15 +96,25 @@ __device__ __forceinline__ uint4 load_vec(const typename E::storage* in_body, in
   }
 }
 
+// |g| p_j of a logit, or of two, by one FMA and one ex2: nK = log2|g| - lse log2(e).
+struct FoldedPower {
+  float c, nK;
+  __device__ __forceinline__ float one(float x) const { return ex2(fmaf(x, c, nK)); }
+  __device__ __forceinline__ float2 two(float2 x) const {
+    const float2 t = __ffma2_rn(x, make_float2(c, c), make_float2(nK, nK));
+    return make_float2(ex2(t.x), ex2(t.y));
+  }
+};
+
 // Stream one row with g != 0: out_j = -sign(g) |g| p_j (NEG: g > 0), accumulating
 // sum_{j != idx} |g| p_j for the idx element.  Returns this thread's partial sum and
-// whether it wrote the idx element.  The gradient is stored with L2 priority evict_first;
+// whether it wrote the idx element.  power: |g| p_j of the logits.  The gradient is stored with L2 priority evict_first;
 // LAST_READ loads the logits with evict_first too.
 // With kept_vecs > 0, body vectors [0, kept_vecs) come from `kept` (a copy the caller made in
 // shared memory) instead of global memory.
-template <class E, int THREADS, int UNROLL, bool SAME_PHASE, bool NEG, bool LAST_READ = false>
+template <class E, int THREADS, int UNROLL, bool SAME_PHASE, bool NEG, bool LAST_READ = false, class P>
 __device__ __forceinline__ float stream_span(const typename E::storage* in, typename E::storage* out,
-                                             const RowSplit& sp, const Span& sn, int idx, float c, float nK,
+                                             const RowSplit& sp, const Span& sn, int idx, const P& power,
                                              bool& owner, const uint4* kept = nullptr, int kept_vecs = 0) {
   constexpr int VEC = E::kVec;
   using S = typename E::storage;
@@ -114,7 +124,7 @@ __device__ __forceinline__ float stream_span(const typename E::storage* in, type
 
   auto scalar = [&](int j) {
     const float x = E::load_scalar_coherent(in + j);
-    const float e = ex2(fmaf(x, c, nK));
+    const float e = power.one(x);
     if (j == idx) owner = true; else q_acc += e;
     E::store_scalar(out + j, NEG ? -e : e);
   };
@@ -124,15 +134,11 @@ __device__ __forceinline__ float stream_span(const typename E::storage* in, type
   const S* in_body = in + sp.head;
   uint4* ob = reinterpret_cast<uint4*>(out + sp.head);
   const int idx_body = idx - sp.head;  // idx relative to the body start
-  const float2 c2 = make_float2(c, c), nK2 = make_float2(nK, nK);
 
   auto process = [&](const uint4& v, int i) {
     float2 e[E::kPairs];
 #pragma unroll
-    for (int q = 0; q < E::kPairs; ++q) {
-      const float2 t = __ffma2_rn(E::pair(v, q), c2, nK2);
-      e[q] = make_float2(ex2(t.x), ex2(t.y));
-    }
+    for (int q = 0; q < E::kPairs; ++q) e[q] = power.two(E::pair(v, q));
     const unsigned k = static_cast<unsigned>(idx_body - i * VEC);
     if (k < static_cast<unsigned>(VEC)) {  // this vector holds idx: leave it out of the sum
       owner = true;
@@ -207,13 +213,13 @@ __global__ void __launch_bounds__(THREADS) rowgrad_kernel(const BwdParams p) {
     const int64_t loc = id64 - p.vocab_start;
     idx = loc >= 0 && loc < V ? static_cast<int>(loc) : -1;
   }
-  const float nK = fmaf(-lse, kLog2e, log2f(fabsf(g)));  // -(lse*log2e - log2|g|)
+  const FoldedPower power{p.c, fmaf(-lse, kLog2e, log2f(fabsf(g)))};  // -(lse*log2e - log2|g|)
   bool owner = false;
   // d_j = -sign(g) |g| p_j: negated when g > 0.  After a GRPO forward this is the row's
   // last read: evict_first.
   const float q_part =
-      g > 0.f ? stream_span<E, THREADS, UNROLL, SAME_PHASE, true, GRPO>(in, out, sp, sn, idx, p.c, nK, owner)
-              : stream_span<E, THREADS, UNROLL, SAME_PHASE, false, GRPO>(in, out, sp, sn, idx, p.c, nK, owner);
+      g > 0.f ? stream_span<E, THREADS, UNROLL, SAME_PHASE, true, GRPO>(in, out, sp, sn, idx, power, owner)
+              : stream_span<E, THREADS, UNROLL, SAME_PHASE, false, GRPO>(in, out, sp, sn, idx, power, owner);
 
   // g (1 - p_idx) = sign(g) * sum_{j != idx} |g| p_j; written by the thread that wrote
   // the idx element's provisional value, so its two stores stay in program order.

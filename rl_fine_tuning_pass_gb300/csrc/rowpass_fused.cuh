@@ -225,11 +225,11 @@ __global__ void __launch_bounds__(THREADS) fused_kernel(const FusedParams q, int
 
   // sweep 2: dlogits (d_j = -sign(g) |g| p_j, and g (1 - p_idx) at idx)
   bool owner = false;
-  const float nK = sh_nK;
+  const FoldedPower power{c, sh_nK};
   const float q_part =
-      g > 0.f ? stream_span<E, THREADS, UNROLL, SAME_PHASE, true, true>(row, out, osp, osn, gidx, c, nK, owner,
+      g > 0.f ? stream_span<E, THREADS, UNROLL, SAME_PHASE, true, true>(row, out, osp, osn, gidx, power, owner,
                                                                          fused_kept, kv)
-              : stream_span<E, THREADS, UNROLL, SAME_PHASE, false, true>(row, out, osp, osn, gidx, c, nK, owner,
+              : stream_span<E, THREADS, UNROLL, SAME_PHASE, false, true>(row, out, osp, osn, gidx, power, owner,
                                                                           fused_kept, kv);
   const float q_total = block_sum_all<THREADS>(q_part);
   if (owner) E::store_scalar(out + gidx, g > 0.f ? q_total : -q_total);

@@ -294,17 +294,45 @@ __global__ void __launch_bounds__(THREADS) pref_terms_kernel(const PrefParams p)
   pref_terms<THREADS>(p, blockIdx.x, sh);
 }
 
+// |g| p_j for fp32 logits.  The log-sum-exp is one fp32 number, whose half step (4.8e-7 of a gradient for one of 8 to
+// 16) a whole row shares, as with every loss here; little is added to it.  In one exponent (FoldedPower, as for
+// bf16 logits, whose gradients are rounded to 2^-9) the sum of lse log2(e) and log2|g| rounds once more for
+// the row, the exponents are as large as the logits and not as their distance from lse, and c's rounding
+// counts by the logit's size: gradients came out 4.7e-7 off, and 4e-5 for logits around 1000.  Here
+//   |g| p_j = 2^t_j K,   t_j = x_j c - A,   K = |g| 2^(A - lse log2(e) + A c_off),
+// with A the whole number above lse log2(e), whose product is formed in two parts, and c_off what c's rounding
+// lost, over c (t_j c_off, below 1e-6, is left out): 3.0e-7, for a product a pair and no time (the pass waits
+// for memory).
+struct SplitPower {
+  float c, nA, K;
+  __device__ __forceinline__ float one(float x) const { return ex2(fmaf(x, c, nA)) * K; }
+  __device__ __forceinline__ float2 two(float2 x) const {
+    const float2 t = __ffma2_rn(x, make_float2(c, c), make_float2(nA, nA));
+    return __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), make_float2(K, K));
+  }
+};
+template <class E>
+__device__ __forceinline__ auto pref_power(const PrefParams& p, float lse, float g) {
+  if constexpr (E::kVec == 8) {
+    return FoldedPower{p.c, fmaf(-lse, kLog2e, log2f(fabsf(g)))};
+  } else {
+    constexpr float kLog2eLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
+    const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eLo, A = ceilf(hi);
+    return SplitPower{p.c, -A, fabsf(g) * exp2f((A - hi) - lo + fmaf(A, p.c_off, kExpLow * kLog2e))};
+  }
+}
+
 // A row with g != 0 whose logits start at another address mod 16 than its gradient (see stream_span,
 // which does the others): -|g| p_j or |g| p_j to every column, and this thread's part of the sum of
 // |g| p_j over the columns but idx.
-template <class E, int THREADS, int UNROLL, bool NEG>
+template <class E, int THREADS, int UNROLL, bool NEG, class P>
 __device__ __forceinline__ float pref_stream_shifted(const typename E::storage* in, typename E::storage* out,
-                                                     const RowSplit& sp, int idx, float c, float nK, bool& owner) {
+                                                     const RowSplit& sp, int idx, const P& power, bool& owner) {
   constexpr int VEC = E::kVec;
   const int tid = threadIdx.x;
   float sum = 0.f;
   auto scalar = [&](int j) {
-    const float e = ex2(fmaf(E::load_scalar(in + j), c, nK));
+    const float e = power.one(E::load_scalar(in + j));
     if (j == idx) owner = true;
     else sum += e;
     E::store_scalar(out + j, NEG ? -e : e);
@@ -325,8 +353,7 @@ __device__ __forceinline__ float pref_stream_shifted(const typename E::storage* 
       const int at = idx_body - j * VEC;
 #pragma unroll
       for (int q = 0; q < E::kPairs; ++q) {
-        const float2 t = __ffma2_rn(E::pair(v[k], q), make_float2(c, c), make_float2(nK, nK));
-        e[q] = make_float2(ex2(t.x), ex2(t.y));
+        e[q] = power.two(E::pair(v[k], q));
         s = __fadd2_rn(s, make_float2(2 * q == at ? 0.f : e[q].x, 2 * q + 1 == at ? 0.f : e[q].y));
       }
       owner |= static_cast<unsigned>(at) < static_cast<unsigned>(VEC);
@@ -353,15 +380,15 @@ __device__ __forceinline__ void pref_grad_row(const PrefParams& p, int64_t b, in
     return;
   }
   const int idx = static_cast<int>(id64);
-  const float nK = fmaf(-lse, kLog2e, log2f(fabsf(g)));
+  const auto power = pref_power<E>(p, lse, g);
   bool owner = false;
   float part;
   if constexpr (SAME_PHASE)
-    part = g > 0.f ? stream_span<E, THREADS, UNROLL, true, true, true>(in, out, sp, sn, idx, p.c, nK, owner)
-                   : stream_span<E, THREADS, UNROLL, true, false, true>(in, out, sp, sn, idx, p.c, nK, owner);
+    part = g > 0.f ? stream_span<E, THREADS, UNROLL, true, true, true>(in, out, sp, sn, idx, power, owner)
+                   : stream_span<E, THREADS, UNROLL, true, false, true>(in, out, sp, sn, idx, power, owner);
   else
-    part = g > 0.f ? pref_stream_shifted<E, THREADS, UNROLL, true>(in, out, sp, idx, p.c, nK, owner)
-                   : pref_stream_shifted<E, THREADS, UNROLL, false>(in, out, sp, idx, p.c, nK, owner);
+    part = g > 0.f ? pref_stream_shifted<E, THREADS, UNROLL, true>(in, out, sp, idx, power, owner)
+                   : pref_stream_shifted<E, THREADS, UNROLL, false>(in, out, sp, idx, power, owner);
   const float total = block_sum_all<THREADS>(part);
   if (owner) E::store_scalar(out + idx, g > 0.f ? total : -total);
 }

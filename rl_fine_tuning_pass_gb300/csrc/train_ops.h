@@ -18,7 +18,7 @@ struct PrefParams {
   const float* dloss;      // [pairs] backward, fused
   float c;                 // log2(e) / T
   float c_fwd;             // the same in the forward: of 15 bits for bf16 logits
-  float c_off;             // (log2(e) / T - c_fwd) / c_fwd
+  float c_off;             // (log2(e) / T - c_fwd) / c_fwd: for fp32 logits what c's rounding lost, over c
   float ln2_hi, ln2_lo;    // 1 / T / c_fwd: what ln2 is to the rounded c
   float inv_hi, inv_lo;    // 1 / T
   float T;
