@@ -629,7 +629,9 @@ typedef struct {
  *   dlogits       as in grpo_loss_bwd (may alias logits exactly).  Rows with a zero factor (masked
  *                 ones; a hinge without loss; dloss == 0) are written as +0.0 and not read
  * An unmasked row whose idx is outside [0, V) sets GRPO_DEVERR_IDX_OUT_OF_RANGE; its logp, its
- * pair's outputs and with them the pair's dlogits are NaN.  The fused call's outputs are those of the
+ * pair's outputs and with them the pair's dlogits are NaN.  So they are for an unmasked row that has no
+ * mass, its largest logit below about -1.2e7 T (-2^24 T / log2(e)): -inf or another mask's value in every column;
+ * its lse is -inf.  The fused call's outputs are those of the
  * forward followed by the backward.
  */
 grpo_status preference_loss_fwd(const grpo_rows* logits, const int64_t* idx, const float* ref_logp,

@@ -133,15 +133,18 @@ __device__ __forceinline__ Stat pref_row(const typename E::storage* row, int V, 
   return Stat{rs.a, rs.s.x + rs.s.y, rs.u.x + rs.u.y};
 }
 
-// logp and lse of a row from its merged statistic (thread 0).
+// logp and lse of a row from its merged statistic (thread 0).  Rows without mass: nothing but -inf, or so far down
+// (a mask's values in every column) that lse has no fraction in fp32 and the backward no digit of any p_j.
+constexpr float kNoMass = -0x1p24f;
 __device__ __forceinline__ void pref_row_outputs(const PrefParams& p, int64_t r, const Stat& st, float x_idx, bool bad) {
-  const float more = st.s > 0.f ? fmaf(p.c_off, kLn2 * st.u / st.s, kExpLow) : 0.f;  // nothing but -inf: ln 0
+  const bool none = st.a <= kNoMass;
+  const float more = none ? 0.f : fmaf(p.c_off, kLn2 * st.u / st.s, kExpLow);
   const TwoSum lse = two_add(two_add(two_mul(st.a, TwoSum{p.ln2_hi, p.ln2_lo}), ln_two_parts(st.s)), TwoSum{more, 0.f});
   const TwoSum logp = two_sub(two_mul(x_idx, TwoSum{p.inv_hi, p.inv_lo}), lse);
-  p.lse[r] = lse.hi + lse.lo;
-  const float rounded = logp.hi + logp.lo;
-  p.logp[r] = bad ? __int_as_float(0x7FC00000) : rounded;
-  p.logp[2 * p.pairs * p.x.L + r] = bad || !isfinite(rounded) ? 0.f : logp.lo - (rounded - logp.hi);
+  p.lse[r] = none ? -INFINITY : lse.hi + lse.lo;
+  const float rounded = bad || none ? __int_as_float(0x7FC00000) : logp.hi + logp.lo;
+  p.logp[r] = rounded;
+  p.logp[2 * p.pairs * p.x.L + r] = !isfinite(rounded) ? 0.f : logp.lo - (rounded - logp.hi);
   if (bad && p.dev_err) atomicOr(p.dev_err, GRPO_DEVERR_IDX_OUT_OF_RANGE_BIT);
 }
 
