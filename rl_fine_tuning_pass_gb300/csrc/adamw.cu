@@ -540,11 +540,11 @@ cudaError_t launch_adamw(AdamwTensor* tensors, int64_t count, const AdamwScalars
     while (end < count && end - at < kAdamwMany && kind_of(tensors[end]) == kind) chunks += chunks_of(tensors[end++]);
     // chunks a CTA: few enough for some sixteen CTAs after one another in each place, which evens out that
     // some SMs are farther from the memory, but four where there are enough of them for every place, so
-    // that the step's beginning and the first loads are a small part; at most 64
+    // that the step's beginning and the first loads are a small part; at most 64 (which 2^32 chunks, the most
+    // that a call may have, come to: 2^26 CTAs)
     const int64_t places = static_cast<int64_t>(sms) * kAdamwCtasPerSm;
     int64_t run = std::max<int64_t>(chunks / (16 * places), std::min<int64_t>(4, chunks / places));
     run = std::min<int64_t>(64, std::max<int64_t>(1, run));
-    while (chunks / run > 0x40000000) run *= 2;  // CTAs are counted in 31 bits
     const Part p{tensors + at, static_cast<int>(end - at), static_cast<uint32_t>(run), end == count};
     cudaError_t e = cudaErrorInvalidValue;
     switch (kind) {
