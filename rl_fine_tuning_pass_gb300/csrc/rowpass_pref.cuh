@@ -48,14 +48,18 @@ __device__ __forceinline__ TwoSum ln_two_parts(float s) {
 //   to the large sum each time (6e-7 for 151936 columns).  So the exponentials of a step are added
 //   to one another first, which takes no more additions;
 // - the exponential: ex2.approx is 5.1e-8 too small on average below 0 (2^24 arguments in [-20, 20), the
-//   same in every octave; 3e-8 of spread around that).  Log-sum-exps came out 2.7e-8 (fp32 logits) to
-//   5.1e-8 (bf16) too small: 4.5e-8 are added;
+//   same in every octave; 3e-8 of spread around that).  Log-sum-exps came out 5.1e-8 (bf16 logits) and 4e-8 (fp32)
+//   too small, which are added: for V = 512 to 151936, T = 0.7 to 1.3 and logits of a spread of 1 or 2 their means over
+//   2048 rows are then within 4e-9 (bf16) and 1.6e-8 (fp32).  With 4.5e-8 for both, bf16 stayed 6e-9 low: 5e-7 of
+//   a reward of 1 over 800 tokens, where the plain sum of such log-probs is 2e-7 off.  (A spread of 4 at T = 0.7 and V =
+//   151936 leaves 8e-8: what small terms lose beside a thread's large ones.)
 // - the rounding of t = x c - a, which is the same for the same bf16 logit in every row: c has 15 bits
 //   for bf16 logits, so that x c is exact (fp32 logits are not alike, and their errors average out);
 // - the rounding of c: x_idx / T is formed in two parts, and the log-sum-exp is corrected to first
 //   order.  With 1 + d the exact log2(e) / T over c, |d| <= 2^-15 (the second order is below 1e-8),
 //   ln sum 2^(x c (1 + d)) = ln2 (1 + d) a + ln s + d ln2 u / s,   u = sum 2^t t.
-constexpr float kExpLow = 4.5e-8f;
+template <class E>
+constexpr float kExpLow = E::kVec == 8 ? 5.1e-8f : 4e-8f;
 
 __device__ __forceinline__ void pref_offset(Running& rs, float newm, float c) {
   newm = fmaxf(newm, kNegClamp);  // columns masked by their type's lowest value: newm * c may be -inf
@@ -136,9 +140,10 @@ __device__ __forceinline__ Stat pref_row(const typename E::storage* row, int V, 
 // logp and lse of a row from its merged statistic (thread 0).  Rows without mass: nothing but -inf, or so far down
 // (a mask's values in every column) that lse has no fraction in fp32 and the backward no digit of any p_j.
 constexpr float kNoMass = -0x1p24f;
+template <class E>
 __device__ __forceinline__ void pref_row_outputs(const PrefParams& p, int64_t r, const Stat& st, float x_idx, bool bad) {
   const bool none = st.a <= kNoMass;
-  const float more = none ? 0.f : fmaf(p.c_off, kLn2 * st.u / st.s, kExpLow);
+  const float more = none ? 0.f : fmaf(p.c_off, kLn2 * st.u / st.s, kExpLow<E>);
   const TwoSum lse = two_add(two_add(two_mul(st.a, TwoSum{p.ln2_hi, p.ln2_lo}), ln_two_parts(st.s)), TwoSum{more, 0.f});
   const TwoSum logp = two_sub(two_mul(x_idx, TwoSum{p.inv_hi, p.inv_lo}), lse);
   p.lse[r] = none ? -INFINITY : lse.hi + lse.lo;
@@ -168,7 +173,7 @@ __device__ __forceinline__ void pref_forward_row(const PrefParams& p, int64_t r,
   const bool bad = id < 0 || id >= V;
   const float x_idx = tid == 0 ? E::load_scalar(row + (bad ? 0 : static_cast<int>(id))) : 0.f;
   const Stat st = stat_block_reduce<THREADS>(mine);
-  if (tid == 0) pref_row_outputs(p, r, st, x_idx, bad);
+  if (tid == 0) pref_row_outputs<E>(p, r, st, x_idx, bad);
 }
 
 template <class E, int THREADS, int UNROLL, bool KEEP>
@@ -321,7 +326,7 @@ __device__ __forceinline__ auto pref_power(const PrefParams& p, float lse, float
   } else {
     constexpr float kLog2eLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
     const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eLo, A = ceilf(hi);
-    return SplitPower{p.c, -A, fabsf(g) * exp2f((A - hi) - lo + fmaf(A, p.c_off, kExpLow * kLog2e))};
+    return SplitPower{p.c, -A, fabsf(g) * exp2f((A - hi) - lo + fmaf(A, p.c_off, kExpLow<E> * kLog2e))};
   }
 }
 
