@@ -616,7 +616,7 @@ typedef struct {
 } grpo_pref_args;
 
 /*
- *   logits        [2P, L, V] bf16 or fp32;  idx [2P*L] int64, read only on unmasked rows
+ *   logits        [2P, L, V] bf16 or fp32;  idx [2P*L] int64, any value on masked rows
  *   ref_logp      [2P] fp32: the reference policy's S_b (a mean if `average`), or NULL = 0
  *   mask          [2P*L] uint8 (0: prompt or padding), or NULL = every token counts
  *   args          HOST struct
@@ -676,7 +676,8 @@ grpo_status grad_norm(const grpo_grad_tensor* tensors, int64_t count, float* nor
  *   p -= lr weight_decay p + lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
  * in fp32 (the moments' products and sums rounded one by one), with t the steps made with `state`,
- * this one included.  A norm that is inf or NaN leaves everything as it is, the step count too.
+ * this one included.  A norm that is inf or NaN leaves everything as it is, the step count too.  Without a norm
+ * a g' that is not finite, or whose square is above fp32's range, makes its v so, and with 8-bit states its block.
  *
  * 8-bit states: each 256 elements of a tensor, from its first, share two scales.  With a code's bits
  * read as those of an fp32 number (sign apart), shifted up by 20 and by 19 places:

@@ -22,7 +22,7 @@ namespace grpo {
 namespace {
 
 constexpr int kNormThreads = 256, kNormPer = 32;
-constexpr int kNormCtasBf16 = 5, kNormCtasF32 = 4;  // an SM (600M bf16: 190 us with 4, 181 with 5, 183 with 6)
+constexpr int kNormCtasBf16 = 5, kNormCtasF32 = 4;  // an SM (600M bf16: 202 us with 4, 187 with 5, 189 with 6)
 constexpr int64_t kNormChunk = kNormThreads * kNormPer;
 
 // A thread's 32 elements of a chunk, as they lie in memory: four vectors of bf16, eight of fp32.

@@ -242,7 +242,7 @@ __device__ __forceinline__ void pref_pair(const PrefParams& p, int64_t i, const 
 }
 
 // Both sequences' sums and the pair's terms, by one CTA, in an order that depends on L alone.  The
-// log-probs are read from L2: in the fused kernel other SMs have just written them.
+// log-probs, each read once, are in L2: the launch before has written them.
 template <int THREADS>
 __device__ __forceinline__ void pref_terms(const PrefParams& p, int64_t i, PairSums<THREADS>& sh) {
   constexpr int kAhead = 4;
@@ -428,7 +428,9 @@ inline int pref_threads(const PrefParams& p, int esize, int64_t rows, int sms) {
 
 // A batch of whose rows L2 holds most until the backward (384 MB with a mask, which leaves a part of the rows, 192
 // without) is read with priority to stay: 4 pairs of 512 tokens at V = 32000 bf16, both passes, 84.6 ->
-// 81.3 us, 3 of 170 at V = 32003 fp32 50.7 -> 45.9; a larger one without: 16 pairs of 512 295 -> 292 us.
+// 81.3 us, 3 of 170 at V = 32003 fp32 50.7 -> 45.9; a larger one without: 16 pairs of 512 295 -> 292 us.  (How much a
+// mask leaves is not known here.  Both passes over 260 and 340 MB at V = 32000 bf16: with priority up to 384 MB 82 and 110
+// us where it leaves three eighths, 138 and 178 where it leaves all; up to 192 MB 87 and 112, 137 and 175.)
 template <class E, int THREADS, int UNROLL>
 cudaError_t launch_pref_rows_threads(const PrefParams& p, int64_t rows, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(rows));
