@@ -43,27 +43,29 @@ __device__ __forceinline__ TwoSum ln_two_parts(float s) {
 // A margin is the difference of two sums of thousands of log-probs, so what errs the same way on
 // every token counts (at 2 x 2048 tokens the rewards came out 1.1e-5 off).  Five things did:
 // - the rescaling of sums when a maximum moves: the offsets a are whole numbers here (the maximum
-//   times c, rounded up), so every rescaling is by a power of two, and exact;
+//   times c, rounded up, and 1), so every rescaling is by a power of two, and exact;
 // - the sums: a bf16 logit that occurs often adds the same number often, and loses the same part of it
 //   to the large sum each time (6e-7 for 151936 columns).  So the exponentials of a step are added
 //   to one another first, which takes no more additions;
-// - the exponential: ex2.approx is 5.1e-8 too small on average below 0 (2^24 arguments in [-20, 20), the
-//   same in every octave; 3e-8 of spread around that).  Log-sum-exps came out 5.1e-8 (bf16 logits) and 4e-8 (fp32)
-//   too small, which are added: for V = 512 to 151936, T = 0.7 to 1.3 and logits of a spread of 1 or 2 their means over
-//   2048 rows are then within 4e-9 (bf16) and 1.6e-8 (fp32).  With 4.5e-8 for both, bf16 stayed 6e-9 low: 5e-7 of
-//   a reward of 1 over 800 tokens, where the plain sum of such log-probs is 2e-7 off.  (A spread of 4 at T = 0.7 and V =
-//   151936 leaves 8e-8: what small terms lose beside a thread's large ones.)
+// - the exponential: ex2.approx is 5.1e-8 too small on average below -1, the same in every octave (3e-8 of
+//   spread around that), but 2.2e-8 in (-1, 0) for arguments of all 24 bits: hence the 1 in the offsets, without
+//   which rows of one large logit err by 2e-8 more than others.  What the log-sum-exps came out too small is added: 5.1e-8
+//   for bf16 logits; for fp32 ones 4.58e-8, a little less, for in a row of few logits at whole distances the
+//   exponential is exact.  Means over 2048 rows, V = 512 to 151936, T = 0.7 to 1.3, logits of a spread of 1 or 2: within
+//   4e-9 for bf16 and 6e-9 for fp32.  (With 4.5e-8 for both and no 1: -8e-9 for bf16 and up to 2.1e-8 for fp32, which is
+//   1.5e-6 of a reward of 1 over 700 tokens, where the plain sum of such log-probs is 3e-7 off.  A spread of 4 at T =
+//   0.7 and V = 151936 leaves 1e-7: what small terms lose beside a thread's large ones.)
 // - the rounding of t = x c - a, which is the same for the same bf16 logit in every row: c has 15 bits
 //   for bf16 logits, so that x c is exact (fp32 logits are not alike, and their errors average out);
 // - the rounding of c: x_idx / T is formed in two parts, and the log-sum-exp is corrected to first
 //   order.  With 1 + d the exact log2(e) / T over c, |d| <= 2^-15 (the second order is below 1e-8),
 //   ln sum 2^(x c (1 + d)) = ln2 (1 + d) a + ln s + d ln2 u / s,   u = sum 2^t t.
 template <class E>
-constexpr float kExpLow = E::kVec == 8 ? 5.1e-8f : 4e-8f;
+constexpr float kExpLow = E::kVec == 8 ? 5.1e-8f : 4.58e-8f;
 
 __device__ __forceinline__ void pref_offset(Running& rs, float newm, float c) {
   newm = fmaxf(newm, kNegClamp);  // columns masked by their type's lowest value: newm * c may be -inf
-  const float a = ceilf(newm * c);
+  const float a = ceilf(newm * c) + 1.f;
   if (rs.s.x != 0.f || rs.s.y != 0.f) {
     const float delta = rs.a - a;
     const float2 al = make_float2(ex2(delta), ex2(delta));
@@ -308,9 +310,9 @@ __global__ void __launch_bounds__(THREADS) pref_terms_kernel(const PrefParams p)
 // the row, the exponents are as large as the logits and not as their distance from lse, and c's rounding
 // counts by the logit's size: gradients came out 4.7e-7 off, and 4e-5 for logits around 1000.  Here
 //   |g| p_j = 2^t_j K,   t_j = x_j c - A,   K = |g| 2^(A - lse log2(e) + A c_off),
-// with A the whole number above lse log2(e), whose product is formed in two parts, and c_off what c's rounding
-// lost, over c (t_j c_off, below 1e-6, is left out): 3.0e-7, for a product a pair and no time (the pass waits
-// for memory).
+// with A the second whole number above lse log2(e) (the first one's power in K), whose product is formed in two
+// parts, and c_off what c's rounding lost, over c (t_j c_off, below 1e-6, is left out): 3.0e-7, for a product a pair
+// and no time (the pass waits for memory).
 struct SplitPower {
   float c, nA, K;
   __device__ __forceinline__ float one(float x) const { return ex2(fmaf(x, c, nA)) * K; }
@@ -326,7 +328,7 @@ __device__ __forceinline__ auto pref_power(const PrefParams& p, float lse, float
   } else {
     constexpr float kLog2eLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
     const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eLo, A = ceilf(hi);
-    return SplitPower{p.c, -A, fabsf(g) * exp2f((A - hi) - lo + fmaf(A, p.c_off, kExpLow<E> * kLog2e))};
+    return SplitPower{p.c, -A - 1.f, 2.f * fabsf(g) * exp2f((A - hi) - lo + fmaf(A, p.c_off, kExpLow<E> * kLog2e))};
   }
 }
 
