@@ -193,7 +193,8 @@ struct PairSums {
 };
 
 // Terms of pair i from its sequences' sums of log-probs and numbers of unmasked tokens.  The margin is a
-// small difference of large sums: in two parts up to there, what follows from it in fp32.
+// small difference of large sums: in two parts up to there, what follows from it in fp32 (the logistic loss from
+// both parts: half a step of a margin of 32 to 64 is 2e-6 of a loss of exp(-h)).
 __device__ __forceinline__ void pref_pair(const PrefParams& p, int64_t i, const TwoSum& sum_w, int n_w,
                                           const TwoSum& sum_l, int n_l, float ref_w, float ref_l) {
   const int64_t w = i, l = p.pairs + i;
@@ -219,9 +220,11 @@ __device__ __forceinline__ void pref_pair(const PrefParams& p, int64_t i, const 
     loss = u * u;
     slope = 2.f * u / p.beta;
   } else {  // -(1-e) log sig(h) - e log sig(-h), from soft = log(1 + exp(-|h|)), which never overflows
-    const float e = p.smoothing;
-    const float ex = expf(-fabsf(h)), soft = log1pf(ex), up = 1.f / (1.f + ex);
-    const float neg = soft + (h < 0.f ? -h : 0.f), pos = soft + (h > 0.f ? h : 0.f);
+    // of h and what its rounding lost, which exp(-|h|) takes by a factor
+    const float e = p.smoothing, rest = isfinite(h) ? (margin.hi - h) + margin.lo : 0.f;
+    const float near = expf(-fabsf(h)), ex = fmaf(near, h >= 0.f ? -rest : rest, near);
+    const float soft = log1pf(ex), up = 1.f / (1.f + ex);
+    const float neg = h < 0.f ? (soft - rest) - h : soft, pos = h > 0.f ? (soft + rest) + h : soft;
     loss = (e < 1.f ? (1.f - e) * neg : 0.f) + (e > 0.f ? e * pos : 0.f);
     slope = e - (h >= 0.f ? ex * up : up);  // e sig(h) - (1-e) sig(-h) = e - sig(-h)
   }
